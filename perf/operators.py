@@ -29,29 +29,29 @@ def listed():
     return [
         # a batch of short chat turns, packed: encoder-sized heads, lengths as in the padded workload of the
         # same shape (64 to 512), fp32 output
-        dict(name="prompt softmax, short turns", op="prompt", alpha=1.0, lens=_pick(3, 32, 64, 512), H=12, Hkv=12, f32=True),
+        dict(name="prompt softmax: short turns", op="prompt", alpha=1.0, lens=_pick(3, 32, 64, 512), H=12, Hkv=12, f32=True),
         # long documents beside each other, four query heads to a key/value head
-        dict(name="prompt softmax, documents", op="prompt", alpha=1.0, lens="8192,4097,2999", H=16, Hkv=4, f32=False),
+        dict(name="prompt softmax: documents", op="prompt", alpha=1.0, lens="8192,4097,2999", H=16, Hkv=4, f32=False),
         # the framework's own weighting over mixed lengths, one token among them
-        dict(name="prompt entmax, mixed", op="prompt", alpha=1.5, lens="4096,2500,1000,513,64,1", H=12, Hkv=12, f32=False),
+        dict(name="prompt entmax: mixed", op="prompt", alpha=1.5, lens="4096,2500,1000,513,64,1", H=12, Hkv=12, f32=False),
         # one user's next token: latency
-        dict(name="token softmax, one user", op="attn", alpha=1.0, n=1, lo=2049, hi=2049, pick=1, H=32, Hkv=8, f32=False),
+        dict(name="token softmax: one user", op="attn", alpha=1.0, n=1, lo=2049, hi=2049, pick=1, H=32, Hkv=8, f32=False),
         # a full serving batch, ragged contexts
-        dict(name="token softmax, batch", op="attn", alpha=1.0, n=64, lo=700, hi=16384, pick=2, H=32, Hkv=8, f32=False),
+        dict(name="token softmax: batch", op="attn", alpha=1.0, n=64, lo=700, hi=16384, pick=2, H=32, Hkv=8, f32=False),
         # one user with a long context, plain heads
-        dict(name="token entmax, one user", op="attn", alpha=1.5, n=1, lo=16384, hi=16384, pick=3, H=12, Hkv=12, f32=True),
+        dict(name="token entmax: one user", op="attn", alpha=1.5, n=1, lo=16384, hi=16384, pick=3, H=12, Hkv=12, f32=True),
         # a serving batch of the framework's own weighting, three query heads to a key/value head
-        dict(name="token entmax, batch", op="attn", alpha=1.5, n=48, lo=500, hi=16000, pick=4, H=12, Hkv=4, f32=False),
+        dict(name="token entmax: batch", op="attn", alpha=1.5, n=48, lo=500, hi=16000, pick=4, H=12, Hkv=4, f32=False),
         # one new token for each running sequence
-        dict(name="append, one token each", op="append", n=64, lo=1, hi=8000, new_lo=1, new_hi=1, pick=5, Hkv=8),
+        dict(name="append: one token each", op="append", n=64, lo=1, hi=8000, new_lo=1, new_hi=1, pick=5, Hkv=8),
         # the keys and values of a batch of prompts
-        dict(name="append, prompts", op="append", n=24, lo=0, hi=900, new_lo=100, new_hi=4096, pick=6, Hkv=8),
+        dict(name="append: prompts", op="append", n=24, lo=0, hi=900, new_lo=100, new_hi=4096, pick=6, Hkv=8),
         # room for the next token of a running batch, after the last drafts were dropped
-        dict(name="pages, next token", op="resize", n=128, lo=1, hi=4000, new=5, pick=7, layers=2, Hkv=4),
+        dict(name="pages: next token", op="resize", n=128, lo=1, hi=4000, new=5, pick=7, layers=2, Hkv=4),
         # beams: sixteen sequences forked four times each, every fork about to write a token of its own
-        dict(name="pages, beams", op="beams", n=16, width=4, lo=60, hi=3000, pick=8, layers=12, Hkv=12),
+        dict(name="pages: beams", op="beams", n=16, width=4, lo=60, hi=3000, pick=8, layers=12, Hkv=12),
         # a fragmented pool packed to its front
-        dict(name="pages, compact", op="compact", pages=2500, share=0.6, pick=9, layers=12, Hkv=8),
+        dict(name="pages: compact", op="compact", pages=2500, share=0.6, pick=9, layers=12, Hkv=8),
     ]
 
 
