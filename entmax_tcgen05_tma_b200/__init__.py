@@ -45,3 +45,13 @@ from ._binding import (  # noqa: F401
     strerror,
     version,
 )
+from ._serving import (  # noqa: F401
+    ENTMAX_PAGE_TOKENS,
+    EntmaxCache,
+    entmax_cache_append,
+    entmax_cache_compact,
+    entmax_cache_fork,
+    entmax_cache_resize,
+    entmax_cache_status,
+    entmax_cache_workspace_size,
+)

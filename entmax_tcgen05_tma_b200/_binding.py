@@ -47,6 +47,12 @@ EXPORTED = (
     "entmax_attn_last_cuda_error",
     "entmax_attn_set_wait_timeout_ns",
     "entmax_attn_version",
+    "entmax_cache_resize",
+    "entmax_cache_workspace_size",
+    "entmax_cache_fork",
+    "entmax_cache_compact",
+    "entmax_cache_append",
+    "entmax_cache_status",
 )
 
 
@@ -112,6 +118,19 @@ def _load_library() -> ctypes.CDLL:
     lib.entmax_attn_set_wait_timeout_ns.argtypes = [ctypes.c_ulonglong]
     lib.entmax_attn_version.restype = i
     lib.entmax_attn_version.argtypes = []
+    ll = ctypes.c_longlong
+    lib.entmax_cache_resize.restype = i
+    lib.entmax_cache_resize.argtypes = [vp, vp, vp, i, vp, vp, sz, vp]
+    lib.entmax_cache_workspace_size.restype = sz
+    lib.entmax_cache_workspace_size.argtypes = [vp]
+    lib.entmax_cache_fork.restype = i
+    lib.entmax_cache_fork.argtypes = [vp, vp, vp, i, vp]
+    lib.entmax_cache_compact.restype = i
+    lib.entmax_cache_compact.argtypes = [vp, vp, vp, sz, vp]
+    lib.entmax_cache_append.restype = i
+    lib.entmax_cache_append.argtypes = [vp, i, vp, ll, vp, ll, vp, vp, i, i, vp]
+    lib.entmax_cache_status.restype = i
+    lib.entmax_cache_status.argtypes = [vp]
     return lib
 
 

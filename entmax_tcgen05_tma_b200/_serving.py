@@ -1,0 +1,227 @@
+"""ctypes binding of the serving path: include/entmax_cache.h and entmax_attn_prompt.
+
+Like _binding.py: argument marshalling only.  A call works on the device of its tensors and, unless a
+stream is given, on that device's current torch stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+
+import torch
+
+from ._binding import ENTMAX_BF16, ENTMAX_F32, ENTMAX_OK, EntmaxError, lib
+
+ENTMAX_PAGE_TOKENS = 64
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_void_p), ("V", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("n_layers", ctypes.c_int), ("n_pages", ctypes.c_int),
+                ("H_kv", ctypes.c_int), ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+def _on(device):
+    """The device made current for the call, where it is not already."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _handle(stream, device) -> int:
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (s.device, device))
+    return int(s.cuda_stream)
+
+
+def _need(name, t, shape, dtype, device):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _rows(name, t, heads, device, dtypes=(torch.bfloat16,)):
+    """Checks a [T, heads, 64] tensor whose tokens may lie apart (a slice of a fused projection) and
+    returns its token stride in elements."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.dim() != 3 or t.shape[2] != 64 or (heads is not None and t.shape[1] != heads):
+        raise ValueError("%s has shape %s, expected [T, %s, 64]" % (name, tuple(t.shape), "heads" if heads is None else heads))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    T, h, _ = t.shape
+    least = 64 * h
+    if T == 0 or h == 0:
+        return max(least, 64)
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (h > 1 and s1 != 64):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    if T == 1:
+        return least
+    if s0 < least:
+        raise ValueError("%s: tokens overlap (stride %d)" % (name, s0))
+    return s0
+
+
+class EntmaxCache:
+    """A paged 8-bit key/value cache (include/entmax_cache.h): a handle on the caller's tensors.
+
+    K, V              float8_e4m3fn [n_layers, n_pages, H_kv, 64, 64]
+    k_scale, v_scale  float32 [n_layers, n_pages, H_kv], powers of two
+    refs              int32 [n_pages], sequences that hold each page
+    table             int32 [n_seqs, max_pages], pages of each sequence
+    lens              int32 [n_seqs], tokens of each sequence
+
+    The tensors are the cache; the handle keeps references to them and must not outlive a change of
+    their storage.  ``EntmaxCache.new`` makes an empty one.
+    """
+
+    __slots__ = ("K", "V", "k_scale", "v_scale", "refs", "table", "lens", "n_layers", "n_pages", "H_kv", "n_seqs",
+                 "max_pages", "device", "_struct", "_ptr", "_ws_bytes")
+
+    def __init__(self, K, V, k_scale, v_scale, refs, table, lens):
+        if not isinstance(K, torch.Tensor) or K.dim() != 5:
+            raise ValueError("K must be a [n_layers, n_pages, H_kv, 64, 64] tensor")
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be a [n_seqs, max_pages] tensor")
+        nl, npg, hk = K.shape[:3]
+        ns, mp = table.shape
+        dev = K.device
+        f8, f32, i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+        for name, t, shape, dt in (("K", K, (nl, npg, hk, 64, 64), f8), ("V", V, (nl, npg, hk, 64, 64), f8),
+                                   ("k_scale", k_scale, (nl, npg, hk), f32), ("v_scale", v_scale, (nl, npg, hk), f32),
+                                   ("refs", refs, (npg,), i32), ("table", table, (ns, mp), i32),
+                                   ("lens", lens, (ns,), i32)):
+            _need(name, t, shape, dt, dev)
+        self.K, self.V, self.k_scale, self.v_scale = K, V, k_scale, v_scale
+        self.refs, self.table, self.lens = refs, table, lens
+        self.n_layers, self.n_pages, self.H_kv, self.n_seqs, self.max_pages = nl, npg, hk, ns, mp
+        self.device = dev
+        self._struct = _CacheStruct(K.data_ptr(), V.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                    refs.data_ptr(), table.data_ptr(), lens.data_ptr(), nl, npg, hk, ns, mp)
+        self._ptr = ctypes.addressof(self._struct)
+        self._ws_bytes = int(lib.entmax_cache_workspace_size(self._ptr))
+
+    @classmethod
+    def new(cls, n_layers: int, n_pages: int, H_kv: int, n_seqs: int, max_pages: int, device="cuda"):
+        """An empty cache: every page free, every sequence of length 0."""
+        dev = torch.device(device)
+        shape = (n_layers, n_pages, H_kv)
+        pool = [torch.zeros(shape + (64, 64), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in "KV"]
+        scale = [torch.zeros(shape, dtype=torch.float32, device=dev) for _ in "KV"]
+        refs = torch.zeros((n_pages,), dtype=torch.int32, device=dev)
+        table = torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=dev)
+        lens = torch.zeros((n_seqs,), dtype=torch.int32, device=dev)
+        return cls(*pool, *scale, refs, table, lens)
+
+
+def _is_cache(cache):
+    if not isinstance(cache, EntmaxCache):
+        raise TypeError("cache must be an EntmaxCache")
+    return cache
+
+
+def _workspace(given, nbytes, device):
+    if given is None:
+        return torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=device)
+    if not isinstance(given, torch.Tensor) or given.device != device or given.numel() * given.element_size() < nbytes:
+        raise ValueError("workspace must be a buffer of at least %d bytes on %s" % (nbytes, device))
+    return given
+
+
+def _raise(st, name):
+    if st != ENTMAX_OK:
+        raise EntmaxError(st, name)
+
+
+def entmax_cache_workspace_size(cache) -> int:
+    """Bytes of device workspace for entmax_cache_resize and entmax_cache_compact."""
+    return _is_cache(cache)._ws_bytes
+
+
+def entmax_cache_resize(cache, seqs, new_lens, short_pages=None, workspace=None, stream=None):
+    """Sets the lengths of the listed sequences: room for new tokens, dropped tokens, 0 to free.  seqs
+    and new_lens are int32 device tensors [n].  Returns the device tensor short_pages (int32 [1]): 0, or
+    the number of free pages that were missing, and then no sequence grew."""
+    c = _is_cache(cache)
+    n = seqs.shape[0] if isinstance(seqs, torch.Tensor) and seqs.dim() == 1 else -1
+    _need("seqs", seqs, (n,), torch.int32, c.device)
+    _need("new_lens", new_lens, (n,), torch.int32, c.device)
+    with _on(c.device):
+        if short_pages is None:
+            short_pages = torch.empty((1,), dtype=torch.int32, device=c.device)
+        else:
+            _need("short_pages", short_pages, (1,), torch.int32, c.device)
+        ws = _workspace(workspace, c._ws_bytes, c.device)
+        _raise(lib.entmax_cache_resize(c._ptr, seqs.data_ptr(), new_lens.data_ptr(), n, short_pages.data_ptr(),
+                                       ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, c.device)),
+               "entmax_cache_resize")
+    return short_pages
+
+
+def entmax_cache_fork(cache, src, dst, stream=None):
+    """Makes each empty sequence dst[i] share the tokens of src[i] (int32 device tensors [n])."""
+    c = _is_cache(cache)
+    n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else -1
+    _need("src", src, (n,), torch.int32, c.device)
+    _need("dst", dst, (n,), torch.int32, c.device)
+    with _on(c.device):
+        _raise(lib.entmax_cache_fork(c._ptr, src.data_ptr(), dst.data_ptr(), n, _handle(stream, c.device)),
+               "entmax_cache_fork")
+
+
+def entmax_cache_compact(cache, used=None, workspace=None, stream=None):
+    """Moves the pages in use to the front of the pool.  Returns the device tensor used (int32 [1]): the
+    number of pages in use; the pages from there on are free."""
+    c = _is_cache(cache)
+    with _on(c.device):
+        if used is None:
+            used = torch.empty((1,), dtype=torch.int32, device=c.device)
+        else:
+            _need("used", used, (1,), torch.int32, c.device)
+        ws = _workspace(workspace, c._ws_bytes, c.device)
+        _raise(lib.entmax_cache_compact(c._ptr, used.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                        _handle(stream, c.device)), "entmax_cache_compact")
+    return used
+
+
+def entmax_cache_append(cache, layer, K, V, seqs, cu, stream=None):
+    """Writes the newest tokens of the listed sequences into one layer.  K, V: bf16 [T, H_kv, 64], tokens
+    cu[i] .. cu[i + 1] - 1 being the last ones of sequence seqs[i] (whose length already counts them:
+    entmax_cache_resize); a token stride is allowed (a slice of a fused projection)."""
+    c = _is_cache(cache)
+    ks = _rows("K", K, c.H_kv, c.device)
+    vs = _rows("V", V, c.H_kv, c.device)
+    if V.shape[0] != K.shape[0]:
+        raise ValueError("K and V have %d and %d tokens" % (K.shape[0], V.shape[0]))
+    n = seqs.shape[0] if isinstance(seqs, torch.Tensor) and seqs.dim() == 1 else -1
+    _need("seqs", seqs, (n,), torch.int32, c.device)
+    _need("cu", cu, (n + 1,), torch.int32, c.device)
+    with _on(c.device):
+        _raise(lib.entmax_cache_append(c._ptr, int(layer), K.data_ptr(), ks, V.data_ptr(), vs, seqs.data_ptr(),
+                                       cu.data_ptr(), n, K.shape[0], _handle(stream, c.device)),
+               "entmax_cache_append")
+
+
+def entmax_cache_status(stream=None, device=None) -> int:
+    """Synchronise the stream and return (and clear) the cache status word of its device."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _on(dev):
+        return int(lib.entmax_cache_status(_handle(stream, dev)))
+
+
+def _out_code(out_dtype):
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("out_dtype must be bfloat16 or float32")
+    return ENTMAX_F32 if out_dtype == torch.float32 else ENTMAX_BF16

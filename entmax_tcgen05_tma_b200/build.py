@@ -14,8 +14,9 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libentmax_attn.so"
-SOURCES = ["abi.cu", "fwd.cu", "fwd_dense.cu", "fwd_softmax.cu", "bwd.cu", "bwd_saved.cu", "bwd_dense.cu"]
-DEPS = SOURCES + ["common.cuh", "dense.cuh", "tau15.cuh", "ptx.cuh", "internal.h"]
+SOURCES = ["abi.cu", "fwd.cu", "fwd_dense.cu", "fwd_softmax.cu", "bwd.cu", "bwd_saved.cu", "bwd_dense.cu",
+           "cache.cu"]
+DEPS = SOURCES + ["common.cuh", "dense.cuh", "tau15.cuh", "ptx.cuh", "internal.h", "cache.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -30,7 +31,7 @@ def _stale() -> bool:
     if not LIB.exists():
         return True
     t = LIB.stat().st_mtime
-    deps = [CSRC / d for d in DEPS] + [ROOT / "include" / "entmax_attn.h"]
+    deps = [CSRC / d for d in DEPS] + sorted((ROOT / "include").glob("*.h"))
     return any(p.stat().st_mtime > t for p in deps)
 
 

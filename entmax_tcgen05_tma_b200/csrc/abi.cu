@@ -148,6 +148,11 @@ cudaError_t convert_inputs(const void* const* src, const void** dst, int count, 
 
 }  // namespace
 
+cudaError_t abi_current_device(int* dev) { return current_device(dev); }
+int abi_record(cudaError_t e) { return record(e); }
+cudaError_t abi_status_ptr(int** out) { return status_ptr(out); }
+unsigned long long abi_timeout_ns() { return timeout_ns(); }
+
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, cudaStream_t stream) {
     const int threads = 256;
     const size_t blocks = std::min<size_t>((n + threads - 1) / threads, 148 * 16);
@@ -157,7 +162,7 @@ cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, cudaStream
 }
 
 cudaError_t ensure_smem_attr(const void* func, int bytes, int slot) {
-    constexpr int SLOTS = 16;
+    constexpr int SLOTS = 32;
     static std::atomic<bool> done[SLOTS][MAX_DEVICES] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

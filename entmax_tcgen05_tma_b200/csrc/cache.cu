@@ -1,0 +1,653 @@
+// cache.cu -- the paged 8-bit key/value cache (include/entmax_cache.h): pages (resize, fork, compact)
+// and the writing of new tokens.  The attention over it is in cache_attn.cu.
+//
+// Page bookkeeping runs on the device, so that a decoding loop needs no host round trip and can be
+// captured into a graph.  Everything that decides which page goes where is deterministic: free pages
+// are taken lowest number first in the order of the caller's list, and atomics only add, subtract or
+// take extremes of integers.
+#include <cuda_bf16.h>
+#include <mutex>
+#include "cache.cuh"
+#include "internal.h"
+
+namespace entmax {
+namespace {
+
+__device__ int g_cache_status;  // ENTMAX_OK or ENTMAX_ERR_ARG since the last read
+
+constexpr int MAX_DEV = 64;
+int* g_cache_status_ptr[MAX_DEV] = {};
+std::mutex g_cache_mu;
+
+cudaError_t cache_status_ptr(int** out) {
+    int dev = 0;
+    cudaError_t e = abi_current_device(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lk(g_cache_mu);
+    if (!g_cache_status_ptr[dev]) {
+        void* p = nullptr;
+        e = cudaGetSymbolAddress(&p, g_cache_status);
+        if (e != cudaSuccess) return e;
+        g_cache_status_ptr[dev] = static_cast<int*>(p);
+    }
+    *out = g_cache_status_ptr[dev];
+    return cudaSuccess;
+}
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+constexpr int MAX_LIST = 4096;   // entries of a resize call
+constexpr int PT = 1024;         // threads of the bookkeeping kernels (one CTA)
+
+// Workspace of the bookkeeping kernels: three lists over the pages, one over the sequences, the list of
+// pages to copy and its length.
+struct PageWs {
+    int* owner;    // [n_seqs]
+    int* a;        // [n_pages]
+    int* b;        // [n_pages]
+    int* c;        // [n_pages]
+    int* pairs;    // [2][MAX_LIST]
+    int* count;    // [1]
+};
+size_t page_ws_ints(int n_seqs, int n_pages) { return (size_t)n_seqs + 3 * (size_t)n_pages + 2 * MAX_LIST + 64; }
+PageWs carve_page_ws(void* base, int n_seqs, int n_pages) {
+    int* p = static_cast<int*>(base);
+    PageWs w;
+    w.count = p;
+    w.pairs = p + 64;
+    w.owner = w.pairs + 2 * MAX_LIST;
+    w.a = w.owner + n_seqs;
+    w.b = w.a + n_pages;
+    w.c = w.b + n_pages;
+    return w;
+}
+
+// Exclusive sum over the CTA of v in thread order; *total gets the sum.  part: 32 ints of shared memory.
+__device__ __forceinline__ int block_scan(int v, int* part, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();  // part may still be read from a call before
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int p = part[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, p, o);
+        if (lane >= o) p += y;
+    }
+    *total = __shfl_sync(0xffffffffu, p, 31);
+    const int before = __shfl_sync(0xffffffffu, p, max(warp - 1, 0));
+    return x - v + (warp ? before : 0);
+}
+
+// ---------------------------------------------------------------------------------------- resize
+// One CTA: the lists are short (a batch's sequences) and the counts of a pool are read once at 4 bytes a
+// page, so latency bounds it, not bandwidth.  Per entry in shared memory: sequence (-1: left out), pages
+// it has and wants, its partly filled last page where that must be copied (-1: not), and the first of its
+// fresh pages.
+__global__ void __launch_bounds__(PT) resize_kernel(const CacheArgs c, const int* __restrict__ seqs,
+                                                    const int* __restrict__ new_lens, int n, int* short_pages,
+                                                    const PageWs ws) {
+    extern __shared__ int sm[];
+    int *s_seq = sm, *s_have = sm + n, *s_want = sm + 2 * n, *s_copy = sm + 3 * n, *s_base = sm + 4 * n;
+    __shared__ int part[32];
+    __shared__ int any_shared;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        *ws.count = 0;
+        any_shared = 0;
+    }
+    // a sequence named twice: its first entry counts
+    for (int i = tid; i < n; i += PT) {
+        const int s = seqs[i], nl = new_lens[i];
+        const bool ok = s >= 0 && s < c.n_seqs && nl >= 0 && nl <= c.max_pages * PAGE;
+        s_seq[i] = ok ? s : -1;
+        s_want[i] = ok ? nl : 0;
+        if (ok) ws.owner[s] = n;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += PT)
+        if (s_seq[i] >= 0) atomicMin(&ws.owner[s_seq[i]], i);
+    __syncthreads();
+    for (int i = tid; i < n; i += PT) {
+        int s = s_seq[i], copy = -1, have = 0, want = 0;
+        if (s >= 0) {
+            const int old = c.lens[s], nl = s_want[i];
+            if (__ldcg(&ws.owner[s]) != i || old < 0 || old > c.max_pages * PAGE) {
+                s = -1;
+            } else {
+                have = pages_of(old);
+                want = pages_of(nl);
+                if (nl > old && old % PAGE != 0) {  // writes on its last page
+                    copy = c.table[(size_t)s * c.max_pages + have - 1];
+                    if (copy < 0 || copy >= c.n_pages) s = -1;
+                }
+            }
+        }
+        if (s < 0) {
+            cache_error(c);
+            copy = -1;
+            have = want = 0;
+        }
+        s_seq[i] = s;
+        s_have[i] = have;
+        s_copy[i] = copy;
+        s_base[i] = s >= 0 ? s_want[i] : 0;  // the new length, until the entry's first page is known
+        s_want[i] = want;
+    }
+    __syncthreads();
+    // shrink: release the pages behind the new end
+    for (int i = warp; i < n; i += PT / 32) {
+        const int s = s_seq[i];
+        if (s < 0) continue;
+        int* row = c.table + (size_t)s * c.max_pages;
+        for (int k = s_want[i] + lane; k < s_have[i]; k += 32) {
+            const int p = row[k];
+            if (p >= 0 && p < c.n_pages) atomicSub(&c.refs[p], 1);
+            else cache_error(c);
+            row[k] = -1;
+        }
+        if (lane == 0 && s_want[i] <= s_have[i] && s_copy[i] < 0) c.lens[s] = s_base[i];  // no growth past its pages
+    }
+    __syncthreads();
+    // shared last pages of growing entries: copied, except that the last entry of the list keeps the page
+    // where all its holders are among the entries
+    for (int i = tid; i < n; i += PT) {
+        const int p = s_copy[i];
+        if (p >= 0) {
+            if (__ldcg(&c.refs[p]) > 1) {
+                ws.a[p] = 0;
+                ws.b[p] = -1;
+                any_shared = 1;
+            }
+        }
+    }
+    __syncthreads();
+    if (any_shared) {
+        for (int i = tid; i < n; i += PT) {
+            const int p = s_copy[i];
+            if (p >= 0 && __ldcg(&c.refs[p]) > 1) {
+                atomicAdd(&ws.a[p], 1);
+                atomicMax(&ws.b[p], i);
+            }
+        }
+        __syncthreads();
+    }
+    int total = 0;
+    for (int i0 = 0; i0 < n; i0 += PT) {
+        const int i = i0 + tid;
+        int need = 0;
+        bool copies = false;
+        if (i < n && s_seq[i] >= 0) {
+            const int p = s_copy[i];
+            if (p >= 0) {
+                const int r = __ldcg(&c.refs[p]);
+                copies = r > 1 && !(__ldcg(&ws.a[p]) == r && __ldcg(&ws.b[p]) == i);
+            }
+            need = max(s_want[i] - s_have[i], 0) + (copies ? 1 : 0);
+        }
+        int sum;
+        const int at = block_scan(need, part, &sum);
+        if (i < n) {
+            if (s_seq[i] >= 0 && (need > 0 || s_copy[i] >= 0)) {
+                // from here on s_copy tells: >= 0 the page to copy, -1 nothing, and the entry grows
+                const int len = s_base[i];
+                s_base[i] = total + at;
+                if (!copies) s_copy[i] = -1;
+                ws.owner[s_seq[i]] = len;  // its new length
+            } else {
+                s_seq[i] = -1;  // done: shrunk, unchanged, or left out
+            }
+        }
+        total += sum;
+    }
+    // the lowest-numbered free pages
+    int found = 0;
+    for (int p0 = 0; p0 < c.n_pages && found < total; p0 += 4 * PT) {
+        int f = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int p = p0 + 4 * tid + q;
+            if (p < c.n_pages && __ldcg(&c.refs[p]) <= 0) f |= 1 << q;
+        }
+        int sum;
+        int at = found + block_scan(__popc(f), part, &sum);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (f >> q & 1) {
+                if (at < total) ws.c[at] = p0 + 4 * tid + q;
+                ++at;
+            }
+        found += sum;
+    }
+    if (tid == 0) *short_pages = max(total - found, 0);
+    if (found < total) return;  // uniform: nothing grows
+    __syncthreads();
+    for (int i = warp; i < n; i += PT / 32) {
+        const int s = s_seq[i];
+        if (s < 0) continue;
+        int* row = c.table + (size_t)s * c.max_pages;
+        const int from = s_copy[i], have = s_have[i];
+        int at = s_base[i];
+        if (from >= 0) {
+            if (lane == 0) {
+                const int to = ws.c[at];
+                const int q = atomicAdd(ws.count, 1);
+                ws.pairs[q] = from;
+                ws.pairs[MAX_LIST + q] = to;
+                atomicSub(&c.refs[from], 1);
+                c.refs[to] = 1;
+                row[have - 1] = to;
+            }
+            ++at;
+        }
+        for (int k = have + lane; k < s_want[i]; k += 32) {
+            const int to = ws.c[at + k - have];
+            c.refs[to] = 1;
+            row[k] = to;
+        }
+        if (lane == 0) c.lens[s] = ws.owner[s];
+    }
+}
+
+// ---------------------------------------------------------------------------------------- copies
+// Copies pages src[j] -> dst[j], j < *count, all layers: for each layer and of K and V a page is
+// H_kv * 4 KB in one piece.  Bound by HBM: 16 KB pieces, 64 bytes in flight per thread.  kRenumber: the
+// pages moved, so table entries that name map[p] >= 0 follow (compact).
+template <bool kRenumber>
+__global__ void __launch_bounds__(256) copy_pages_kernel(const CacheArgs c, const int* __restrict__ src,
+                                                         const int* __restrict__ dst, const int* __restrict__ count,
+                                                         const int* __restrict__ map) {
+    const int n = *count;
+    if (kRenumber) {
+        const size_t cells = (size_t)c.n_seqs * c.max_pages;
+        for (size_t k = (size_t)blockIdx.x * 256 + threadIdx.x; k < cells; k += (size_t)gridDim.x * 256) {
+            const int p = c.table[k];
+            if (p >= 0 && p < c.n_pages) {
+                const int to = map[p];
+                if (to >= 0) c.table[k] = to;
+            }
+        }
+    }
+    const size_t piece = 16384, bytes = (size_t)c.Hkv * BLOCK_BYTES;
+    const size_t per = (bytes + piece - 1) / piece;  // pieces of a page's layer
+    const size_t total = (size_t)n * c.n_layers * 2 * per;
+    for (size_t u = blockIdx.x; u < total; u += gridDim.x) {
+        const size_t q = u % per;
+        size_t r = u / per;
+        const int t = (int)(r & 1);
+        r >>= 1;
+        const int layer = (int)(r % c.n_layers), j = (int)(r / c.n_layers);
+        const size_t from = c.block(layer, src[j], 0), to = c.block(layer, dst[j], 0);
+        uint8_t* pool = t ? c.V : c.K;
+        const uint4* a = reinterpret_cast<const uint4*>(pool + from * BLOCK_BYTES + q * piece);
+        uint4* b = reinterpret_cast<uint4*>(pool + to * BLOCK_BYTES + q * piece);
+        const int m = (int)(min(piece, bytes - q * piece) / 16);
+        uint4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (threadIdx.x + 256 * k < m) x[k] = __ldcs(a + threadIdx.x + 256 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (threadIdx.x + 256 * k < m) b[threadIdx.x + 256 * k] = x[k];
+        if (q == 0) {
+            float* sc = t ? c.vs : c.ks;
+            for (int h = threadIdx.x; h < c.Hkv; h += 256) sc[to + h] = sc[from + h];
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------- compact
+// One CTA: counts the pages in use, then pairs the used pages at or above that count with the free pages
+// below it, both in order.  ws.a, ws.b: the pairs; ws.c: the page's new number or -1.
+__global__ void __launch_bounds__(PT) compact_plan_kernel(const CacheArgs c, int* used_out, const PageWs ws) {
+    __shared__ int part[32];
+    const int tid = threadIdx.x;
+    int mine = 0;
+    for (int p = tid; p < c.n_pages; p += PT) mine += c.refs[p] > 0 ? 1 : 0;
+    int used;
+    block_scan(mine, part, &used);
+    int nsrc = 0, ndst = 0;
+    for (int p0 = 0; p0 < c.n_pages; p0 += PT) {
+        const int p = p0 + tid;
+        const int r = p < c.n_pages ? c.refs[p] : 0;
+        const bool src = p < c.n_pages && p >= used && r > 0, dst = p < c.n_pages && p < used && r <= 0;
+        int sum;
+        const int at = block_scan((src ? 1 : 0) | (dst ? 1 << 16 : 0), part, &sum);
+        if (src) ws.a[nsrc + (at & 0xffff)] = p;
+        if (dst) ws.b[ndst + (at >> 16)] = p;
+        if (p < c.n_pages) ws.c[p] = -1;
+        nsrc += sum & 0xffff;
+        ndst += sum >> 16;
+    }
+    __syncthreads();
+    for (int k = tid; k < nsrc; k += PT) {  // as many used pages at or above `used` as free ones below
+        const int from = ws.a[k], to = ws.b[k];
+        ws.c[from] = to;
+        c.refs[to] = c.refs[from];
+        c.refs[from] = 0;
+    }
+    if (tid == 0) {
+        *used_out = used;
+        *ws.count = nsrc;
+    }
+}
+
+// ---------------------------------------------------------------------------------------- fork
+// One CTA per entry.
+__global__ void __launch_bounds__(256) fork_kernel(const CacheArgs c, const int* __restrict__ src,
+                                                   const int* __restrict__ dst, int n) {
+    const int i = blockIdx.x, tid = threadIdx.x;
+    const int s = src[i], d = dst[i];
+    bool bad = s < 0 || s >= c.n_seqs || d < 0 || d >= c.n_seqs;
+    for (int j = tid; j < n && !bad; j += 256) {
+        const int e = dst[j];
+        bad = e == s || (j < i && e == d);
+    }
+    int len = 0;
+    if (!__syncthreads_or(bad)) {
+        len = c.lens[s];
+        bad = c.lens[d] != 0 || len < 0 || len > c.max_pages * PAGE;
+        const int* from = c.table + (size_t)s * c.max_pages;
+        if (!bad)
+            for (int k = tid; k < pages_of(len); k += 256) bad |= from[k] < 0 || from[k] >= c.n_pages;
+    } else {
+        bad = true;
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) cache_error(c);
+        return;
+    }
+    const int* from = c.table + (size_t)s * c.max_pages;
+    int* to = c.table + (size_t)d * c.max_pages;
+    for (int k = tid; k < pages_of(len); k += 256) {
+        const int p = from[k];
+        to[k] = p;
+        atomicAdd(&c.refs[p], 1);
+    }
+    if (tid == 0) c.lens[d] = len;
+}
+
+// ---------------------------------------------------------------------------------------- append
+// First page item of entry i: entry i touches at most (m + 126) / 64 pages for its m tokens, so items
+// (cu_i + 126 i) / 64 .. are its own (the differences of these are at least that).
+__device__ __forceinline__ long long item_base(int cu, int i) { return ((long long)cu + 126ll * i) / 64; }
+long long item_bound(int n, int T) { return ((long long)T + 126ll * n) / 64 + 1; }
+
+// The entry that item w belongs to: the last i in [0, n) with item_base(i) <= w, by a 33-ary search of the
+// warp (cu does not decrease).
+__device__ __forceinline__ int find_entry(const int* __restrict__ cu, int n, long long w) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;  // the answer lies in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 32) / 33;
+        const int i = lo + (lane + 1) * step;
+        const bool ok = i < hi && item_base(cu[i], i) <= w;
+        const int k = __popc(__ballot_sync(0xffffffffu, ok));  // probes that hold come first
+        const int next = min(hi, lo + (k + 1) * step);
+        lo += k * step;
+        hi = next;
+    }
+    return lo;
+}
+
+// One warp per (page, K or V, head) block.  A new token's row of a head is 128 bytes in and 64 bytes out: 8
+// lanes read and write a row, 16 bytes and 8 bytes each, so a warp moves four rows per step and holds a
+// whole block's new rows in registers between the largest-value pass and the conversion.  Bound by HBM
+// for prompts (2 bytes read, 1 written per number) and by the chain of index loads for single tokens.
+__global__ void __launch_bounds__(256) append_kernel(const CacheArgs c, int layer, const uint16_t* __restrict__ K,
+                                                     long long k_stride, const uint16_t* __restrict__ V,
+                                                     long long v_stride, const int* __restrict__ seqs,
+                                                     const int* __restrict__ cu, int n, int T, long long items) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * 8 + warp;
+    const int per = 2 * c.Hkv;
+    const long long item = w / per;
+    if (item >= items) return;
+    const int rest = (int)(w - item * per), is_v = rest >= c.Hkv, head = rest - (is_v ? c.Hkv : 0);
+    const int i = find_entry(cu, n, item);
+    const int c0 = cu[i], c1 = cu[i + 1], s = seqs[i];
+    const long long k = item - item_base(c0, i);
+    if (c0 == c1 || k < 0) return;
+    bool bad = c0 < 0 || c1 < c0 || c1 > T || s < 0 || s >= c.n_seqs;
+    if (!bad) {
+        for (int j = lane; j < i; j += 32) bad |= seqs[j] == s;
+        bad = __any_sync(0xffffffffu, bad);
+    }
+    int len = 0, start = 0, page = 0;
+    long long pg = 0;
+    if (!bad) {
+        len = c.lens[s];
+        start = len - (c1 - c0);
+        bad = start < 0 || len > c.max_pages * PAGE;
+    }
+    if (!bad) {
+        pg = start / PAGE + k;
+        if (pg * PAGE >= len) return;
+        page = c.table[(size_t)s * c.max_pages + pg];
+        bad = page < 0 || page >= c.n_pages || c.refs[page] != 1;
+    }
+    if (bad) {
+        if (lane == 0) cache_error(c);
+        return;
+    }
+    const int p0 = (int)pg * PAGE;
+    const int a = max(start - p0, 0), b = min(len - p0, PAGE);  // rows a .. b - 1 are new, rows before a stay
+    const size_t blk = c.block(layer, page, head);
+    uint8_t* rows = (is_v ? c.V : c.K) + blk * BLOCK_BYTES;
+    float* scale = (is_v ? c.vs : c.ks) + blk;
+    const long long stride = is_v ? v_stride : k_stride;
+    const uint16_t* in = (is_v ? V : K) + (long long)(c0 + p0 - start) * stride + head * 64;  // row r at r * stride, r >= a
+
+    const int r0 = lane >> 3, ch = lane & 7;
+    uint4 x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const int r = r0 + 4 * j;
+        x[j] = make_uint4(0, 0, 0, 0);
+        if (r >= a && r < b) x[j] = __ldg(reinterpret_cast<const uint4*>(in + (long long)r * stride) + ch);
+    }
+    const float old = a > 0 ? *scale : 0.f;
+    // largest magnitude as bf16 bits (their order is that of the magnitudes); infinities and NaN become NaN
+    // and do not count
+    uint32_t m2 = 0;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) m2 = __vmaxu2(m2, v[q] & 0x7fff7fffu);
+    }
+    uint32_t top = max(m2 & 0xffffu, m2 >> 16);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (top >= 0x7f80u) {
+        top = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t lo = v[q] & 0x7fffu, hi = (v[q] >> 16) & 0x7fffu;
+                if (lo >= 0x7f80u) v[q] |= 0x0040u;
+                else top = max(top, lo);
+                if (hi >= 0x7f80u) v[q] |= 0x00400000u;
+                else top = max(top, hi);
+            }
+            x[j] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+    }
+    // smallest power of two 2^e with top / 2^e <= 448 = 1.75 * 2^8 (top = 1.f * 2^(E - 127), f above 0.75 needs
+    // one more); at least 2^-100, and at least the scale of rows that stay
+    int e = max((int)(top >> 7) - 135 + ((top & 0x7fu) > 0x60u ? 1 : 0), -100);
+    if (top < 0x80u) e = -100;
+    float s_new = __uint_as_float((uint32_t)(e + 127) << 23);
+    if (a > 0 && old > s_new) s_new = old;
+    const float inv = 1.f / s_new;  // a power of two: exact
+    if (a > 0 && old < s_new) {     // the rows that stay move to the larger scale
+        const float f = old * inv;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const int r = r0 + 4 * j;
+            if (r < a) {
+                uint2* at = reinterpret_cast<uint2*>(rows + r * 64) + ch;
+                uint2 v = *at;
+                uint16_t o[4];
+                const uint16_t src[4] = {(uint16_t)v.x, (uint16_t)(v.x >> 16), (uint16_t)v.y, (uint16_t)(v.y >> 16)};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t h = e4m3x2_to_f16x2(src[q]);
+                    const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                    o[q] = f32x2_to_e4m3x2(g.x * f, g.y * f);
+                }
+                *at = make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
+            }
+        }
+    }
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0 && !(a > 0 && old >= s_new)) *scale = s_new;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        const int r = r0 + 4 * j;
+        if (r >= a && r < b) {
+            const uint32_t v[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+            uint16_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o[q] = f32x2_to_e4m3x2(__uint_as_float(v[q] << 16) * inv, __uint_as_float(v[q] & 0xffff0000u) * inv);
+            *(reinterpret_cast<uint2*>(rows + r * 64) + ch) = make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
+        }
+    }
+}
+
+}  // namespace
+
+int cache_args(const entmax_cache* c, CacheArgs* out) {
+    if (!c) return ENTMAX_ERR_ARG;
+    if (c->n_layers < 1 || c->n_pages < 1 || c->H_kv < 1 || c->n_seqs < 1 || c->max_pages < 1) return ENTMAX_ERR_ARG;
+    if (!c->K || !c->V || !c->k_scale || !c->v_scale || !c->refs || !c->table || !c->lens) return ENTMAX_ERR_ARG;
+    if (!aligned(c->K, 16) || !aligned(c->V, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+        !aligned(c->refs, 4) || !aligned(c->table, 4) || !aligned(c->lens, 4))
+        return ENTMAX_ERR_ARG;
+    // lengths are 32-bit, and a page's number times its heads indexes scales with 64 bits
+    if (c->max_pages > (1 << 24) || c->n_pages > (1 << 28) || c->H_kv > 1024 || c->n_layers > 65535)
+        return ENTMAX_ERR_UNSUPPORTED;
+    int* status = nullptr;
+    const int rc = abi_record(cache_status_ptr(&status));
+    if (rc) return rc;
+    *out = CacheArgs{static_cast<uint8_t*>(c->K), static_cast<uint8_t*>(c->V), c->k_scale, c->v_scale, c->refs, c->table,
+                     c->lens, c->n_layers, c->n_pages, c->H_kv, c->n_seqs, c->max_pages, status};
+    return ENTMAX_OK;
+}
+
+}  // namespace entmax
+
+using namespace entmax;
+
+namespace {
+constexpr int COPY_GRID = 148 * 8;
+// The cache's host-side checks without the look-up of the device status word (no CUDA call).
+int check_list(const void* a, const void* b, int n, int most) {
+    if (n < 0) return ENTMAX_ERR_ARG;
+    if (n > most) return ENTMAX_ERR_UNSUPPORTED;
+    if (n > 0 && (!a || !b || !aligned(a, 4) || !aligned(b, 4))) return ENTMAX_ERR_ARG;
+    return ENTMAX_OK;
+}
+int check_ws(const entmax_cache* c, const void* ws, size_t bytes) {
+    if (!ws || bytes < entmax_cache_workspace_size(c)) return ENTMAX_ERR_WORKSPACE;
+    return aligned(ws, 16) ? ENTMAX_OK : ENTMAX_ERR_ARG;
+}
+}  // namespace
+
+extern "C" {
+
+size_t entmax_cache_workspace_size(const entmax_cache* c) {
+    if (!c || c->n_seqs < 1 || c->n_pages < 1) return 0;
+    return (page_ws_ints(c->n_seqs, c->n_pages) * sizeof(int) + 255) & ~size_t(255);
+}
+
+int entmax_cache_resize(const entmax_cache* c, const int32_t* seqs, const int32_t* new_lens, int n,
+                        int32_t* short_pages, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    int rc = check_list(seqs, new_lens, n, MAX_LIST);
+    if (rc) return rc;
+    if (!short_pages || !aligned(short_pages, 4)) return ENTMAX_ERR_ARG;
+    rc = check_ws(c, workspace, ws_bytes);
+    if (rc) return rc;
+    CacheArgs a;
+    rc = cache_args(c, &a);
+    if (rc) return rc;
+    const PageWs ws = carve_page_ws(workspace, c->n_seqs, c->n_pages);
+    const int smem = 5 * n * (int)sizeof(int);
+    rc = abi_record(ensure_smem_attr(reinterpret_cast<const void*>(resize_kernel), 5 * MAX_LIST * (int)sizeof(int), 16));
+    if (rc) return rc;
+    resize_kernel<<<1, PT, smem, stream>>>(a, seqs, new_lens, n, short_pages, ws);
+    rc = abi_record(cudaGetLastError());
+    if (rc || n == 0) return rc;
+    copy_pages_kernel<false><<<COPY_GRID, 256, 0, stream>>>(a, ws.pairs, ws.pairs + MAX_LIST, ws.count, nullptr);
+    return abi_record(cudaGetLastError());
+}
+
+int entmax_cache_fork(const entmax_cache* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream) {
+    int rc = check_list(src, dst, n, 65535);
+    if (rc) return rc;
+    CacheArgs a;
+    rc = cache_args(c, &a);
+    if (rc || n == 0) return rc;
+    fork_kernel<<<n, 256, 0, stream>>>(a, src, dst, n);
+    return abi_record(cudaGetLastError());
+}
+
+int entmax_cache_compact(const entmax_cache* c, int32_t* used, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+    if (!used || !aligned(used, 4)) return ENTMAX_ERR_ARG;
+    int rc = check_ws(c, workspace, ws_bytes);
+    if (rc) return rc;
+    CacheArgs a;
+    rc = cache_args(c, &a);
+    if (rc) return rc;
+    const PageWs ws = carve_page_ws(workspace, c->n_seqs, c->n_pages);
+    compact_plan_kernel<<<1, PT, 0, stream>>>(a, used, ws);
+    rc = abi_record(cudaGetLastError());
+    if (rc) return rc;
+    copy_pages_kernel<true><<<COPY_GRID, 256, 0, stream>>>(a, ws.a, ws.b, ws.count, ws.c);
+    return abi_record(cudaGetLastError());
+}
+
+int entmax_cache_append(const entmax_cache* c, int layer, const void* K, long long k_stride, const void* V,
+                        long long v_stride, const int32_t* seqs, const int32_t* cu, int n, int T, cudaStream_t stream) {
+    int rc = check_list(seqs, cu, n, 1 << 20);
+    if (rc) return rc;
+    if (!c || T < 0) return ENTMAX_ERR_ARG;
+    if (layer < 0 || layer >= c->n_layers) return ENTMAX_ERR_ARG;
+    if (T > 0 && (!K || !V || !aligned(K, 16) || !aligned(V, 16) || k_stride % 8 || v_stride % 8 ||
+                  k_stride < 64ll * c->H_kv || v_stride < 64ll * c->H_kv))
+        return ENTMAX_ERR_ARG;
+    CacheArgs a;
+    rc = cache_args(c, &a);
+    if (rc || n == 0 || T == 0) return rc;
+    const long long items = item_bound(n, T), warps = items * 2 * c->H_kv;
+    if ((warps + 7) / 8 > 0x7fffffffll) return ENTMAX_ERR_UNSUPPORTED;
+    append_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a, layer, static_cast<const uint16_t*>(K), k_stride,
+                                                                  static_cast<const uint16_t*>(V), v_stride, seqs, cu,
+                                                                  n, T, items);
+    return abi_record(cudaGetLastError());
+}
+
+int entmax_cache_status(cudaStream_t stream) {
+    int* p = nullptr;
+    int rc = abi_record(cache_status_ptr(&p));
+    if (rc) return rc;
+    rc = abi_record(cudaStreamSynchronize(stream));
+    if (rc) return rc;
+    int v = 0;
+    rc = abi_record(cudaMemcpy(&v, p, sizeof(int), cudaMemcpyDeviceToHost));
+    if (rc) return rc;
+    const int zero = 0;
+    rc = abi_record(cudaMemcpy(p, &zero, sizeof(int), cudaMemcpyHostToDevice));
+    return rc ? rc : v;
+}
+
+}  // extern "C"

@@ -131,6 +131,13 @@ cudaError_t launch_fwd_dense(const AttnArgs& a, const FwdOut& o, cudaStream_t st
 cudaError_t launch_bwd_dense(const AttnArgs& a, const BwdIO& io, cudaStream_t stream);
 cudaError_t launch_f32_to_bf16(const float* src, void* dst, size_t n, cudaStream_t stream);
 
+// abi.cu: the calling thread's device with a context current on it; ENTMAX_ERR_CUDA with the error
+// recorded, or ENTMAX_OK; the device status word; the launches' wait bound.
+cudaError_t abi_current_device(int* dev);
+int abi_record(cudaError_t e);
+cudaError_t abi_status_ptr(int** out);
+unsigned long long abi_timeout_ns();
+
 // Raises a kernel's dynamic shared-memory limit once per (kernel slot, device).
 cudaError_t ensure_smem_attr(const void* func, int bytes, int slot);
 

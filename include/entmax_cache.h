@@ -1,0 +1,113 @@
+/*
+ * entmax_cache.h -- C ABI of the serving path: a paged key/value cache held in 8 bits, and the
+ * attention of single tokens over it.  (Prompts: entmax_attn_prompt in entmax_attn.h.)
+ *
+ * The AdaSplash pages describe encoders and a causal decoder layer that recompute every key and
+ * value; they print no cache.  The weights are those of the other entry points: for query head h of
+ * a token, with the keys j of its sequence's cached tokens,
+ *   S_j = scale <Q_h, K_j>,  p = 1.5-entmax(S) or softmax(S) (alpha),  O_h = sum_j p_j V_j,
+ * and query head h reads key/value head h / (H / H_kv).
+ *
+ * Format.  A page holds the keys and values of 64 consecutive tokens of one sequence, for every layer
+ * and key/value head.  A block is one page's [64 tokens][64] numbers of one layer and head, in e4m3
+ * (1 sign, 4 exponent, 3 mantissa bits, largest 448), with one scale: the value is number * scale.
+ * Scales are powers of two, the smallest with max|x| / scale <= 448 over the block's tokens (at least
+ * 2^-100): e4m3 is a floating-point format, so a power of two costs no accuracy above its subnormal
+ * numbers, the division is exact, and when a token with a larger value joins a partly filled
+ * block, the numbers already there move to the new scale exactly (down to subnormals, which round
+ * to nearest even).
+ *
+ * Errors.  Arguments are checked on the host as in entmax_attn.h.  Indices that live on the device
+ * (sequences, pages, lengths) are checked by the kernels: an entry of a list that names no sequence,
+ * names one twice where that is not allowed, or whose table or length is out of range is left out,
+ * nothing of it is read or written, and the device's cache status word records ENTMAX_ERR_ARG
+ * (entmax_cache_status).  All calls are asynchronous on `stream`; calls that change a cache, and calls
+ * that read what they change, have to be ordered by the caller (one stream, or events).
+ */
+#ifndef ENTMAX_CACHE_H
+#define ENTMAX_CACHE_H
+
+#include "entmax_attn.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define ENTMAX_PAGE_TOKENS 64
+
+/* A cache: device buffers owned by the caller, and their sizes.  The struct itself is read during the
+ * call only.  Tables, lengths and reference counts are shared by all layers. */
+typedef struct entmax_cache {
+    void* K;           /* [n_layers][n_pages][H_kv][64][64] e4m3, 16-byte aligned */
+    void* V;           /* the same */
+    float* k_scale;    /* [n_layers][n_pages][H_kv] */
+    float* v_scale;    /* the same */
+    int32_t* refs;     /* [n_pages] sequences that hold the page; 0: free.  Start: all 0 */
+    int32_t* table;    /* [n_seqs][max_pages] page of the sequence's tokens 64 k .. 64 k + 63; only the
+                          entries that its length needs are read, the others are -1 where this library wrote them */
+    int32_t* lens;     /* [n_seqs] tokens; 0: an empty slot.  Start: all 0 */
+    int n_layers, n_pages, H_kv, n_seqs, max_pages;
+} entmax_cache;
+
+/*
+ * Sets the lengths of n sequences: room for new tokens, dropping rejected ones, freeing (length 0).
+ *   seqs, new_lens  device int32 [n]; every sequence at most once, 0 <= new_len <= 64 max_pages.
+ *   short_pages     device int32 [1]: 0, or how many free pages were missing.
+ * Sequences that shrink release the pages behind their new end first (a page is free again when its
+ * last holder releases it).  Sequences that grow then take the lowest-numbered free pages in the order of
+ * the list.  A growing sequence whose last page is partly filled and shared (entmax_cache_fork) gets a
+ * copy of that page, all layers; where all holders of the page grow in the same call, the last of
+ * the list keeps it.  If the free pages do not suffice, no sequence grows (shrinking took effect) and
+ * *short_pages says how many are missing.  New tokens hold nothing until entmax_cache_append
+ * wrote them, layer by layer.  Pages behind a sequence's end keep their contents.
+ *   workspace       device buffer of entmax_cache_workspace_size(c) bytes, 16-byte aligned.
+ * n <= 4096 (else ENTMAX_ERR_UNSUPPORTED).
+ */
+ENTMAX_API int entmax_cache_resize(const entmax_cache* c, const int32_t* seqs, const int32_t* new_lens, int n,
+                                   int32_t* short_pages, void* workspace, size_t ws_bytes, cudaStream_t stream);
+
+/* Workspace of entmax_cache_resize and entmax_cache_compact; 0 for an invalid cache. */
+ENTMAX_API size_t entmax_cache_workspace_size(const entmax_cache* c);
+
+/*
+ * Makes sequence dst[i] (empty) hold the tokens of src[i], sharing its pages.  A source may be named
+ * several times; a destination once, and it is no source of the same call.  n <= 65535.
+ */
+ENTMAX_API int entmax_cache_fork(const entmax_cache* c, const int32_t* src, const int32_t* dst, int n,
+                                 cudaStream_t stream);
+
+/*
+ * Moves the pages in use to the front of the pool: with U pages in use, the k-th used page numbered U
+ * or above moves to the k-th free page below U; tables and counts follow.  Afterwards pages U .. are
+ * free (they keep their contents).
+ *   used        device int32 [1]: U.
+ *   workspace   as entmax_cache_resize.
+ */
+ENTMAX_API int entmax_cache_compact(const entmax_cache* c, int32_t* used, void* workspace, size_t ws_bytes,
+                                    cudaStream_t stream);
+
+/*
+ * Writes the keys and values of the newest tokens of n sequences into one layer.
+ *   K, V        bf16, token t's head h at [t * stride + 64 h]: contiguous [T][H_kv][64] for a stride of
+ *               64 H_kv; strides in elements, multiples of 8, at least 64 H_kv; 16-byte aligned.
+ *   cu          device int32 [n + 1], cu[0] = 0, not decreasing, cu[n] <= T: tokens cu[i] .. cu[i + 1] - 1 are
+ *               the last cu[i + 1] - cu[i] tokens of sequence seqs[i] (its length already counts them).
+ *   seqs        device int32 [n], every sequence at most once.
+ * Tokens of T behind cu[n] are not read.  A block that holds tokens from before keeps them, moved to
+ * the larger scale where the new tokens need one.  Infinite and NaN elements are stored as NaN and do not
+ * count for the scale.  A page that other sequences hold too is not written (ENTMAX_ERR_ARG on the
+ * device): entmax_cache_resize gives a growing sequence a page of its own.
+ */
+ENTMAX_API int entmax_cache_append(const entmax_cache* c, int layer, const void* K, long long k_stride, const void* V,
+                                   long long v_stride, const int32_t* seqs, const int32_t* cu, int n, int T,
+                                   cudaStream_t stream);
+
+/* Synchronises `stream`, then returns and clears the cache status word of the current device: ENTMAX_OK,
+ * or ENTMAX_ERR_ARG if a kernel left an entry out since the last read. */
+ENTMAX_API int entmax_cache_status(cudaStream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* ENTMAX_CACHE_H */

@@ -1,0 +1,102 @@
+"""Host-side checks of the cache entry points (no GPU): bad arguments are refused before any CUDA call; the
+pointers are never dereferenced on the host.  And the tests' own model against hand-made numbers."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import entmax_tcgen05_tma_b200 as E
+from entmax_tcgen05_tma_b200._serving import _CacheStruct
+from cache_model import VALUES, Model, block_exp, to_e4m3
+
+P = 0x10000
+
+
+def cache(**kw):
+    a = dict(K=P, V=P, k_scale=P, v_scale=P, refs=P, table=P, lens=P, n_layers=2, n_pages=8, H_kv=3, n_seqs=4, max_pages=5)
+    a.update(kw)
+    return _CacheStruct(*[a[f] for f, _ in _CacheStruct._fields_])
+
+
+def call(name, c, **kw):
+    p = None if c is None else ctypes.addressof(c)
+    a = dict(seqs=P, lens=P, n=1, short=P, ws=P, ws_bytes=1 << 20, layer=0, K=P, V=P, ks=192, vs=192, cu=P, T=4)
+    a.update(kw)
+    return {
+        "resize": lambda: E.lib.entmax_cache_resize(p, a["seqs"], a["lens"], a["n"], a["short"], a["ws"], a["ws_bytes"], None),
+        "fork": lambda: E.lib.entmax_cache_fork(p, a["seqs"], a["lens"], a["n"], None),
+        "compact": lambda: E.lib.entmax_cache_compact(p, a["short"], a["ws"], a["ws_bytes"], None),
+        "append": lambda: E.lib.entmax_cache_append(p, a["layer"], a["K"], a["ks"], a["V"], a["vs"], a["seqs"], a["cu"], a["n"], a["T"], None),
+    }[name]()
+
+
+@pytest.mark.parametrize("name", ["resize", "fork", "compact", "append"])
+@pytest.mark.parametrize("kw,code", [
+    (dict(K=None), E.ENTMAX_ERR_ARG), (dict(V=P + 8), E.ENTMAX_ERR_ARG), (dict(k_scale=None), E.ENTMAX_ERR_ARG),
+    (dict(v_scale=P + 2), E.ENTMAX_ERR_ARG), (dict(refs=None), E.ENTMAX_ERR_ARG), (dict(table=P + 1), E.ENTMAX_ERR_ARG),
+    (dict(lens=None), E.ENTMAX_ERR_ARG), (dict(n_layers=0), E.ENTMAX_ERR_ARG), (dict(n_pages=0), E.ENTMAX_ERR_ARG),
+    (dict(H_kv=0), E.ENTMAX_ERR_ARG), (dict(n_seqs=-1), E.ENTMAX_ERR_ARG), (dict(max_pages=0), E.ENTMAX_ERR_ARG),
+    (dict(max_pages=(1 << 24) + 1), E.ENTMAX_ERR_UNSUPPORTED), (dict(H_kv=1025), E.ENTMAX_ERR_UNSUPPORTED),
+])
+def test_bad_caches(name, kw, code):
+    more = dict(ks=64 * 1025, vs=64 * 1025) if kw.get("H_kv", 0) > 1024 else {}
+    assert call(name, cache(**kw), **more) == code
+    assert call(name, None) in (E.ENTMAX_ERR_ARG, E.ENTMAX_ERR_WORKSPACE)
+
+
+@pytest.mark.parametrize("name,kw,code", [
+    ("resize", dict(n=-1), E.ENTMAX_ERR_ARG), ("resize", dict(n=4097), E.ENTMAX_ERR_UNSUPPORTED),
+    ("resize", dict(seqs=None), E.ENTMAX_ERR_ARG), ("resize", dict(lens=P + 2), E.ENTMAX_ERR_ARG),
+    ("resize", dict(short=None), E.ENTMAX_ERR_ARG), ("resize", dict(ws=None), E.ENTMAX_ERR_WORKSPACE),
+    ("resize", dict(ws_bytes=16), E.ENTMAX_ERR_WORKSPACE), ("resize", dict(ws=P + 4), E.ENTMAX_ERR_ARG),
+    ("fork", dict(n=65536), E.ENTMAX_ERR_UNSUPPORTED), ("fork", dict(lens=None), E.ENTMAX_ERR_ARG),
+    ("fork", dict(n=-3), E.ENTMAX_ERR_ARG), ("compact", dict(short=None), E.ENTMAX_ERR_ARG),
+    ("compact", dict(ws=None), E.ENTMAX_ERR_WORKSPACE), ("append", dict(layer=2), E.ENTMAX_ERR_ARG),
+    ("append", dict(layer=-1), E.ENTMAX_ERR_ARG), ("append", dict(K=None), E.ENTMAX_ERR_ARG),
+    ("append", dict(V=P + 8), E.ENTMAX_ERR_ARG), ("append", dict(ks=191), E.ENTMAX_ERR_ARG),
+    ("append", dict(vs=128), E.ENTMAX_ERR_ARG), ("append", dict(ks=196), E.ENTMAX_ERR_ARG),
+    ("append", dict(T=-1), E.ENTMAX_ERR_ARG), ("append", dict(cu=None), E.ENTMAX_ERR_ARG),
+    ("append", dict(n=-1), E.ENTMAX_ERR_ARG),
+])
+def test_bad_arguments(name, kw, code):
+    assert call(name, cache(), **kw) == code
+
+
+def test_workspace_size_grows_with_the_pool():
+    small, large = cache(n_pages=8), cache(n_pages=100000)
+    a, b = (E.lib.entmax_cache_workspace_size(ctypes.addressof(x)) for x in (small, large))
+    assert 0 < a < b and a % 256 == b % 256 == 0 and b - a < 13 * 100000
+    assert E.lib.entmax_cache_workspace_size(None) == 0
+
+
+def test_binding_refuses_cpu_tensors():
+    z = torch.zeros
+    with pytest.raises(ValueError):
+        E.EntmaxCache(z(1, 2, 1, 64, 64, dtype=torch.uint8).view(torch.float8_e4m3fn),
+                      z(1, 2, 1, 64, 64, dtype=torch.uint8).view(torch.float8_e4m3fn), z(1, 2, 1), z(1, 2, 1),
+                      z(2, dtype=torch.int32), z(1, 1, dtype=torch.int32), z(1, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        E.entmax_cache_compact(None)
+
+
+def test_model_numbers():
+    assert np.nanmax(VALUES) == 448 and np.isnan(VALUES[0x7f]) and np.isnan(VALUES[0xff])
+    finite = VALUES[np.isfinite(VALUES)]
+    np.testing.assert_array_equal(to_e4m3(finite), finite)
+    assert to_e4m3(17.0) == 16 and to_e4m3(19.0) == 20 and to_e4m3(2.0 ** -10) == 0 and to_e4m3(1.5 * 2.0 ** -9) == 2.0 ** -8
+    x = torch.linspace(-448, 448, 4001, dtype=torch.float64)
+    np.testing.assert_array_equal(to_e4m3(x.numpy()), x.float().to(torch.float8_e4m3fn).double().numpy())
+    assert block_exp(np.array([448.0])) == 0 and block_exp(np.array([448.5])) == 1 and block_exp(np.zeros(3)) == -100
+    assert block_exp(np.array([np.inf, np.nan, 7.0])) == -6
+
+
+def test_model_pages():
+    m = Model(1, 4, 1, 3, 3)
+    assert m.resize([0], [65]) == 0 and m.table[0] == [0, 1, -1]
+    m.fork([0], [2])
+    assert m.refs == [2, 2, 0, 0]
+    assert m.resize([2], [66]) == 0 and m.table[2] == [0, 2, -1] and m.refs == [2, 1, 1, 0]
+    assert m.resize([0], [0]) == 0 and m.refs == [1, 0, 1, 0]
+    assert m.compact() == 2 and m.table[2] == [0, 1, -1] and m.refs == [1, 1, 0, 0]
+    assert m.resize([1], [192]) == 1 and m.lens == [0, 0, 66]

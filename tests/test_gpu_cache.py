@@ -1,0 +1,274 @@
+"""Pages and writes of the 8-bit cache against a plain model, on the GPU."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from cache_model import VALUES, Model
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def make(n_layers=2, n_pages=24, H_kv=3, n_seqs=10, max_pages=8):
+    import entmax_tcgen05_tma_b200 as E
+    return E.EntmaxCache.new(n_layers, n_pages, H_kv, n_seqs, max_pages), Model(n_layers, n_pages, H_kv, n_seqs, max_pages)
+
+
+def numbers(pool):
+    return VALUES[pool.view(torch.uint8).cpu().numpy()]
+
+
+def same_pages(c, m):
+    assert c.lens.tolist() == m.lens
+    assert c.refs.tolist() == m.refs
+    assert c.table.tolist() == m.table
+
+
+def same_tokens(c, m):
+    """Every block of a page in use: numbers and scales bit for bit, up to the holders' lengths."""
+    num = [numbers(c.K), numbers(c.V)]
+    scale = [c.k_scale.cpu().numpy().astype(np.float64), c.v_scale.cpu().numpy().astype(np.float64)]
+    for s, n in enumerate(m.lens):
+        for k in range(0, n, PAGE):
+            p, rows = m.table[s][k // PAGE], min(PAGE, n - k)
+            for a, b, f, g in zip(num, m.num, scale, m.scale):
+                np.testing.assert_array_equal(a[:, p, :, :rows], b[:, p, :, :rows])
+                np.testing.assert_array_equal(f[:, p], g[:, p])
+
+
+def write(c, m, layer, seqs, new, rng, spread=1.0):
+    """Random new tokens for every listed sequence (their lengths already count them)."""
+    import entmax_tcgen05_tma_b200 as E
+    cu = [0]
+    for x in new:
+        cu.append(cu[-1] + x)
+    g = torch.Generator().manual_seed(rng.randrange(1 << 30))
+    T, H = cu[-1] + 2, c.H_kv  # two tokens behind the last: not read
+    kv = torch.randn((T, 2 * H, 64), generator=g) * torch.exp2(spread * torch.randn((T, 2 * H, 1), generator=g))
+    kv[cu[-1]:] = float("nan")
+    kv = kv.to(torch.bfloat16)
+    d = kv.cuda()
+    E.entmax_cache_append(c, layer, d[:, :H], d[:, H:], ints(seqs), ints(cu))
+    x = kv.double().numpy()
+    m.append(layer, x[:, :H], x[:, H:], seqs, cu)
+
+
+def resize(c, m, seqs, lens):
+    import entmax_tcgen05_tma_b200 as E
+    short = E.entmax_cache_resize(c, ints(seqs), ints(lens))
+    want = m.resize(seqs, lens)
+    assert short.item() == want
+    same_pages(c, m)
+    return want
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_use(seed):
+    """Growing, writing, forking, dropping, freeing and compacting in random order."""
+    import entmax_tcgen05_tma_b200 as E
+    rng = random.Random(seed)
+    c, m = make(n_pages=rng.choice([9, 24, 40]))
+    missing = 0
+    for step in range(40):
+        what = rng.random()
+        live = [s for s, n in enumerate(m.lens) if n > 0]
+        empty = [s for s, n in enumerate(m.lens) if n == 0]
+        if what < 0.5:
+            seqs = rng.sample(range(len(m.lens)), rng.randint(1, 5))
+            old = [m.lens[s] for s in seqs]
+            new = [min(512, n + rng.choice([0, 1, 1, 2, 63, 64, 65, rng.randint(0, 200)])) for n in old]
+            if resize(c, m, seqs, new):
+                missing += 1
+                continue
+            for layer in range(2):
+                write(c, m, layer, seqs, [b - a for a, b in zip(old, new)], rng)
+        elif what < 0.7 and live:
+            seqs = rng.sample(live, rng.randint(1, len(live)))
+            resize(c, m, seqs, [rng.choice([0, n, max(0, n - 1), rng.randint(0, n)]) for n in (m.lens[s] for s in seqs)])
+        elif what < 0.85 and live and empty:
+            dst = rng.sample(empty, rng.randint(1, len(empty)))
+            src = [rng.choice(live) for _ in dst]
+            E.entmax_cache_fork(c, ints(src), ints(dst))
+            m.fork(src, dst)
+            same_pages(c, m)
+        else:
+            used = E.entmax_cache_compact(c)
+            assert used.item() == m.compact()
+            same_pages(c, m)
+        same_tokens(c, m)
+    assert E.entmax_cache_status() == 0
+
+
+def test_missing_pages_leave_all_as_it_was():
+    c, m = make(n_pages=4)
+    assert resize(c, m, [0, 1], [100, 64]) == 0
+    assert resize(c, m, [0, 1, 2], [129, 64, 65]) == 2   # three pages wanted, one free
+    assert resize(c, m, [0, 1, 2], [128, 0, 65]) == 0    # sequence 1 gives its page up first
+    assert resize(c, m, [0, 2], [0, 0]) == 0
+    assert m.refs == [0] * 4
+
+
+def test_all_holders_grow_and_the_last_keeps_the_page():
+    import entmax_tcgen05_tma_b200 as E
+    rng = random.Random(3)
+    c, m = make()
+    resize(c, m, [4], [70])
+    write(c, m, 0, [4], [70], rng)
+    write(c, m, 1, [4], [70], rng)
+    E.entmax_cache_fork(c, ints([4, 4, 4]), ints([1, 2, 3]))
+    m.fork([4, 4, 4], [1, 2, 3])
+    resize(c, m, [4, 3, 1, 2], [71, 72, 200, 71])
+    assert m.table[2][1] == 1  # the page of tokens 64 .. 69 stayed with the last of the list
+    same_tokens(c, m)
+    for layer in range(2):
+        write(c, m, layer, [4, 3, 1, 2], [1, 2, 130, 1], rng)
+    same_tokens(c, m)
+
+
+@pytest.mark.parametrize("spread", [0.0, 6.0])
+@pytest.mark.parametrize("H_kv", [1, 2, 5, 16])
+def test_blocks_filled_in_pieces(H_kv, spread):
+    """One block written in pieces of 1, 2, 31, 29 and 1 tokens; with a large spread its scale keeps growing."""
+    rng = random.Random(H_kv)
+    c, m = make(n_layers=1, H_kv=H_kv)
+    at = 0
+    for step in (1, 2, 31, 29, 1, 1, 64, 100):
+        at += step
+        resize(c, m, [7], [at])
+        write(c, m, 0, [7], [step], rng, spread)
+        same_tokens(c, m)
+
+
+def test_values_out_of_the_ordinary():
+    """Zeros, the smallest and largest bf16 numbers, infinities and NaN."""
+    import entmax_tcgen05_tma_b200 as E
+    c, m = make(n_layers=1, H_kv=1, n_pages=12)
+    tiny, huge = torch.finfo(torch.bfloat16).smallest_normal, torch.finfo(torch.bfloat16).max
+    sets = [[0.0, -0.0], [tiny, -tiny, tiny / 64], [huge, -huge, 1.0], [float("inf"), 1.0, float("-inf")],
+            [float("nan"), 3.0], [448.0, 449.0], [450.0, 1e-3], [2.0 ** -92 * 1.75, 2.0 ** -93]]
+    for s, vals in enumerate(sets):
+        x = torch.zeros(66, 1, 64)
+        x.view(-1)[:len(vals)] = torch.tensor(vals)
+        x[65, 0, 0] = vals[0]
+        x = x.to(torch.bfloat16)
+        resize(c, m, [s], [66])
+        E.entmax_cache_append(c, 0, x.cuda(), -x.cuda(), ints([s]), ints([0, 66]))
+        m.append(0, x.double().numpy(), -x.double().numpy(), [s], [0, 66])
+        same_tokens(c, m)
+        resize(c, m, [s], [0])
+
+
+def test_tokens_behind_the_end_stay_and_lists_may_be_empty():
+    import entmax_tcgen05_tma_b200 as E
+    rng = random.Random(0)
+    c, m = make(n_layers=1, H_kv=2)
+    c.K.view(torch.uint8).fill_(0x7f)  # NaN everywhere
+    resize(c, m, [0, 1, 2], [70, 0, 64])
+    write(c, m, 0, [0, 1, 2], [70, 0, 64], rng)
+    same_tokens(c, m)
+    raw = c.K.view(torch.uint8)
+    assert (raw[0, 1, :, 6:] == 0x7f).all() and (raw[0, 3:] == 0x7f).all()
+    before = raw.clone()
+    none = ints([])
+    E.entmax_cache_append(c, 0, torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda"),
+                          torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda"), none, ints([0]))
+    E.entmax_cache_fork(c, none, none)
+    assert E.entmax_cache_resize(c, none, none).item() == 0
+    same_pages(c, m)
+    assert torch.equal(before, raw) and E.entmax_cache_status() == 0
+
+
+def test_entries_that_name_nothing_valid_are_left_out():
+    """Out-of-range and repeated sequences, lengths and pages: nothing of them changes, the status word tells."""
+    import entmax_tcgen05_tma_b200 as E
+    rng = random.Random(1)
+    c, m = make(n_layers=1)
+    resize(c, m, [0, 1], [100, 64])
+    write(c, m, 0, [0, 1], [100, 64], rng)
+
+    def told(code=E.ENTMAX_ERR_ARG):
+        assert E.entmax_cache_status() == code
+        assert E.entmax_cache_status() == 0
+        same_pages(c, m)
+        same_tokens(c, m)
+
+    E.entmax_cache_resize(c, ints([-1, 10, 2, 3]), ints([1, 1, -1, 8 * 64 + 1]))
+    told()
+    E.entmax_cache_resize(c, ints([2, 0, 2]), ints([10, 100, 70]))   # sequence 2 twice: the first counts
+    m.resize([2], [10])
+    m.append(0, np.zeros((10, 3, 64)), np.zeros((10, 3, 64)), [2], [0, 10])
+    z = torch.zeros(10, 3, 64, dtype=torch.bfloat16, device="cuda")
+    E.entmax_cache_append(c, 0, z, z, ints([2]), ints([0, 10]))
+    told()
+    E.entmax_cache_fork(c, ints([0, 0, 1, 99, 4, 5]), ints([1, 0, 12, 3, -1, 5]))
+    told()
+    E.entmax_cache_fork(c, ints([0, 1, 6, 0]), ints([6, 6, 7, 8]))   # 6 twice (the first counts), 6 as a source
+    m.fork([0, 0], [6, 8])
+    told()
+    # a page that another sequence holds too, more tokens than the sequence has, tokens behind T, a page out
+    # of range, a sequence twice
+    x = torch.ones(70, 3, 64, dtype=torch.bfloat16, device="cuda")
+    for seqs, cu in (([6], [0, 1]), ([2], [0, 11]), ([2], [0, 71]), ([77], [0, 1]), ([2], [5, 3])):
+        E.entmax_cache_append(c, 0, x, x, ints(seqs), ints(cu))
+        told()
+    E.entmax_cache_append(c, 0, x, x, ints([2, 2]), ints([0, 1, 2]))
+    m.append(0, np.ones((1, 3, 64)), np.ones((1, 3, 64)), [2], [0, 1])
+    told()
+    kept = c.table[2, 0].item()
+    for bad in (-1, 24, 1 << 30):
+        c.table[2, 0] = m.table[2][0] = bad
+        E.entmax_cache_append(c, 0, x, x, ints([2]), ints([0, 1]))
+        E.entmax_cache_fork(c, ints([2]), ints([9]))
+        E.entmax_cache_resize(c, ints([2]), ints([12]))
+        assert E.entmax_cache_status() == E.ENTMAX_ERR_ARG
+        same_pages(c, m)
+    c.table[2, 0] = m.table[2][0] = kept
+    same_tokens(c, m)
+
+
+def test_captured_steps_follow_the_lengths():
+    """A captured resize + append, replayed: every replay takes the lengths and tokens it finds."""
+    import entmax_tcgen05_tma_b200 as E
+    rng = random.Random(2)
+    c, m = make(n_layers=1, H_kv=2)
+    seqs, lens, cu = [3, 0, 5], [5, 63, 64], [0, 1, 2, 3]
+    resize(c, m, seqs, lens)
+    write(c, m, 0, seqs, lens, rng)
+    d_seqs, d_lens, d_cu = ints(seqs), ints(lens), ints(cu)
+    x = torch.zeros(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    short = torch.zeros(1, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        d_lens.add_(1)
+        E.entmax_cache_resize(c, d_seqs, d_lens, short_pages=short)
+        E.entmax_cache_append(c, 0, x[:, :2], x[:, 2:], d_seqs, d_cu)
+    for step in range(3):
+        new = torch.randn(3, 4, 64, generator=torch.Generator().manual_seed(step)).to(torch.bfloat16)
+        x.copy_(new)
+        g.replay()
+        lens = [n + 1 for n in lens]
+        assert m.resize(seqs, lens) == short.item() == 0
+        m.append(0, new[:, :2].double().numpy(), new[:, 2:].double().numpy(), seqs, cu)
+        same_pages(c, m)
+        same_tokens(c, m)
+    assert E.entmax_cache_status() == 0
+
+
+def test_large_lists_and_pools():
+    """4096 sequences in one call; a pool of 20011 pages."""
+    rng = random.Random(9)
+    c, m = make(n_layers=1, H_kv=1, n_pages=20011, n_seqs=4100, max_pages=9)
+    seqs = rng.sample(range(4100), 4096)
+    lens = [rng.randint(0, 300) for _ in seqs]
+    assert resize(c, m, seqs, lens) == 0
+    rng.shuffle(seqs)
+    assert resize(c, m, seqs, [rng.randint(0, 576) for _ in seqs]) >= 0
+    import entmax_tcgen05_tma_b200 as E
+    assert E.entmax_cache_compact(c).item() == m.compact()
+    same_pages(c, m)
