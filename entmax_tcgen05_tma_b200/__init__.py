@@ -49,6 +49,8 @@ from ._serving import (  # noqa: F401
     ENTMAX_PAGE_TOKENS,
     EntmaxCache,
     entmax_cache_append,
+    entmax_cache_attn,
+    entmax_cache_attn_workspace_size,
     entmax_cache_compact,
     entmax_cache_fork,
     entmax_cache_resize,

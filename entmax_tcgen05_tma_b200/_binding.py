@@ -52,6 +52,8 @@ EXPORTED = (
     "entmax_cache_fork",
     "entmax_cache_compact",
     "entmax_cache_append",
+    "entmax_cache_attn",
+    "entmax_cache_attn_workspace_size",
     "entmax_cache_status",
 )
 
@@ -129,6 +131,10 @@ def _load_library() -> ctypes.CDLL:
     lib.entmax_cache_compact.argtypes = [vp, vp, vp, sz, vp]
     lib.entmax_cache_append.restype = i
     lib.entmax_cache_append.argtypes = [vp, i, vp, ll, vp, ll, vp, vp, i, i, vp]
+    lib.entmax_cache_attn.restype = i
+    lib.entmax_cache_attn.argtypes = [vp, i, vp, ll, vp, i, i, f, f, i, vp, i, vp, vp, sz, vp]
+    lib.entmax_cache_attn_workspace_size.restype = sz
+    lib.entmax_cache_attn_workspace_size.argtypes = [i, i, i, f]
     lib.entmax_cache_status.restype = i
     lib.entmax_cache_status.argtypes = [vp]
     return lib

@@ -225,3 +225,39 @@ def _out_code(out_dtype):
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("out_dtype must be bfloat16 or float32")
     return ENTMAX_F32 if out_dtype == torch.float32 else ENTMAX_BF16
+
+
+def entmax_cache_attn_workspace_size(n: int, H: int, H_kv: int, alpha: float = 1.5) -> int:
+    """Bytes of device workspace for entmax_cache_attn on n tokens."""
+    return int(lib.entmax_cache_attn_workspace_size(int(n), int(H), int(H_kv), float(alpha)))
+
+
+def entmax_cache_attn(cache, layer, Q, seqs, max_len, scale=None, alpha=1.5, out_dtype=torch.bfloat16, O=None,
+                      tau=None, workspace=None, stream=None):
+    """Attention of one token of each listed sequence over all of its cached tokens in one layer.
+
+    Q: bf16 [n, H, 64] (a token stride is allowed); seqs: int32 device tensor [n]; max_len: no listed
+    sequence is longer (the cache's capacity, 64 * max_pages, always holds); alpha 1.5 or 1 (softmax).
+    Returns (O, tau): O [n, H, 64] in ``out_dtype``, tau [n, H] fp32."""
+    c = _is_cache(cache)
+    qs = _rows("Q", Q, None, c.device)
+    n, H, D = Q.shape
+    if H % c.H_kv != 0:
+        raise ValueError("H (%d) must be a multiple of the cache's H_kv (%d)" % (H, c.H_kv))
+    _need("seqs", seqs, (n,), torch.int32, c.device)
+    code = _out_code(out_dtype)
+    with _on(c.device):
+        if O is None:
+            O = torch.empty((n, H, D), dtype=out_dtype, device=c.device)
+        else:
+            _need("O", O, (n, H, D), out_dtype, c.device)
+        if tau is None:
+            tau = torch.empty((n, H), dtype=torch.float32, device=c.device)
+        else:
+            _need("tau", tau, (n, H), torch.float32, c.device)
+        ws = _workspace(workspace, lib.entmax_cache_attn_workspace_size(n, H, c.H_kv, float(alpha)), c.device)
+        _raise(lib.entmax_cache_attn(c._ptr, int(layer), Q.data_ptr(), qs, seqs.data_ptr(), n, int(max_len),
+                                     float(D ** -0.5 if scale is None else scale), float(alpha), H, O.data_ptr(), code,
+                                     tau.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                     _handle(stream, c.device)), "entmax_cache_attn")
+    return O, tau

@@ -1,0 +1,1123 @@
+// cache_attn.cu -- attention of single tokens over the paged 8-bit cache (include/entmax_cache.h).
+//
+// For one token and query head, with its sequence's N cached keys: S_j = scale <q, K_j>, p = softmax(S) or
+// 1.5-entmax(S), O = sum_j p_j V_j.  A key is read for 64 products per query head that shares it, so the
+// cache's bytes bound the operation: K and V once (128 bytes per token and key/value head), and for
+// 1.5-entmax K alone, since the values of a few dozen keys suffice.
+//
+// Work.  A unit is one page (64 keys) of one (token, key/value head, group of at most 8 of its query heads).
+// All units, in that order, are dealt to the warps of a persistent grid in equal contiguous runs, counted
+// on the device from the cache's lengths: ragged batches balance, and a captured launch follows the
+// lengths it finds.  A warp's run is cut into segments at the row ends; a row that lies in one run is
+// finished there (softmax), any other is joined by a second kernel from its segments in order.
+//
+// Warps work alone: each keeps a ring of pages in shared memory (cp.async, 16 bytes a lane, chunks of 16
+// bytes swizzled within a row so that all fragment reads are free of bank conflicts), and multiplies with
+// mma.sync m16n8k16.  The tensor work is 1/16 of what the bytes allow at the issue rate of mma.sync, the
+// operands have to pass through registers anyway (e4m3 to fp16, exact), and 8 query heads fill N = 8, where
+// tcgen05 would use 8 of its smallest 128 x 16 tile; so the warp-level product is the fitting one here.
+//   S^T = K q^T: keys are the M side, heads the N side.  q goes to fp16 by a power of two per head, exact for
+//   values within 2^-26 of the head's largest.  A lane's 16 consecutive bytes of a key row serve its four
+//   K = 16 steps: the products' order over d is a permutation that q shares.
+//   O^T = V^T P^T: V's rows are paired byte by byte (prmt) into (key, key') fragments; P^T comes from S^T by
+//   an 8 x 8 transpose (movmatrix).  P enters as two fp16 parts (the rounded weight and the rounded rest: 22
+//   bits) after a shift of 2^15, so a weight down to 2^-18 of the row's largest keeps them all; one part
+//   would leave errors of 2^-11, twelve times what an fp32 output may have.  Sums, maxima and O are held in fp32.
+#include <cuda_bf16.h>
+#include <math.h>
+#include <algorithm>
+#include "cache.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace entmax {
+namespace {
+
+constexpr int WARPS = 8;              // per CTA, one CTA per SM
+constexpr int GRID = 148;
+constexpr int MAX_TOKENS = 4096;      // tokens (rows of Q) of a call: their page counts lie in shared memory
+constexpr int HG = 8;                 // query heads of a group
+constexpr float P_SHIFT = 15.f;       // softmax weights enter the product times 2^15
+constexpr float LOG2E_F = 1.4426950408889634f, LN2_F = 0.6931471805599453f;
+
+struct TokArgs {
+    CacheArgs c;
+    const __nv_bfloat16* Q;  // token i, head h at i * q_stride + 64 h
+    long long q_stride;
+    const int* seqs;
+    int n, H, G, groups;     // G = H / H_kv query heads share a key/value head, in `groups` groups of at most 8
+    int layer, max_len;
+    float scale;
+    void* O;                 // [n][H][64]
+    int out_f32;
+    float* tau;              // [n][H]
+    int warps;               // of the grid
+    // workspace
+    int* prefix;             // [n + 1] pages before token i
+    float* part_o;           // softmax: [warps][2][8][64] sum of 2^(x - m) V
+    float2* part_ml;         // softmax: [warps][2][8] m (log2 units), sum of 2^(x - m)
+    int heads;               // query heads of a full group, min(G, 8)
+    int* cand_n;             // entmax: [warps + rows][heads] candidates listed; -1 too many, -2 not finite.
+                             // The segment of row r (token, key/value head, group) in warp w: w + r
+    float* cand_cut;         // entmax: the same, lower bound of tau that they were cut at
+    float2* cand;            // entmax: the same [GC], (score, key as int bits)
+};
+constexpr int GC = 128;      // candidates of a segment and head
+
+// Units of the call and the warps that share them.
+struct Deal {
+    long long units;
+    int warps;
+    __device__ __forceinline__ long long start(int w) const { return units * w / warps; }
+    __device__ __forceinline__ int owner(long long u) const { return (int)(((u + 1) * warps - 1) / units); }
+};
+__device__ __forceinline__ Deal deal_of(const TokArgs& a, int pages) {
+    Deal d;
+    d.units = (long long)pages * a.c.Hkv * a.groups;
+    d.warps = (int)min((long long)a.warps, d.units);
+    return d;
+}
+
+// Tokens of the sequence of row i; -1 where its number or length is out of range.
+__device__ __forceinline__ int row_len(const TokArgs& a, int i) {
+    const int s = a.seqs[i];
+    if (s < 0 || s >= a.c.n_seqs) return -1;
+    const int len = a.c.lens[s];
+    return len < 0 || len > a.max_len ? -1 : len;
+}
+
+// Exclusive prefix of the rows' page counts into pre[0 .. n] (whole CTA); CTA 0 leaves it in the workspace
+// and reports rows out of range.
+__device__ __forceinline__ void page_prefix(const TokArgs& a, int* pre) {
+    __shared__ int part[WARPS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int carry = 0;
+    for (int i0 = 0; i0 < a.n; i0 += WARPS * 32) {
+        const int i = i0 + tid;
+        const int len = i < a.n ? row_len(a, i) : 0;
+        if (len < 0 && blockIdx.x == 0) cache_error(a.c);
+        int x = len > 0 ? pages_of(len) : 0;
+        const int v = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) part[warp] = x;
+        __syncthreads();
+        int before = carry, all = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const int p = part[w];
+            if (w < warp) before += p;
+            all += p;
+        }
+        if (i < a.n) {
+            pre[i] = before + x - v;
+            if (blockIdx.x == 0) a.prefix[i] = before + x - v;
+        }
+        carry += all;
+    }
+    if (tid == 0) {
+        pre[a.n] = carry;
+        if (blockIdx.x == 0) a.prefix[a.n] = carry;
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+// Maximum that keeps a NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Lane (g, t) = (lane / 4, lane % 4) of a product.  Row of a 16-key tile that the product's key index k
+// (0 .. 7; the upper half adds 8) names: 0 1 3 2 4 5 7 6.  Rows of even and odd index then alternate over
+// both halves of a 128-byte line for K's reads (k = g) and for V's (k = 2 t, 2 t + 1) alike.
+__device__ __forceinline__ int key_row(int k) { return k ^ ((k >> 1) & 1); }
+// Byte offset of 16-byte chunk c of row r in a page's block in shared memory.
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4)); }
+
+// Lane's share of a 4 KB block into shared memory.
+__device__ __forceinline__ void load_block(uint32_t dst, const uint8_t* src, int lane) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int idx = lane + 32 * j;
+        cp_async16(dst + chunk_at(idx >> 2, idx & 3), src + 16 * idx);
+    }
+}
+
+// Fragments of q for a group's heads: lane (g, t) holds head g's dimensions 16 t .. 16 t + 15 as fp16 times a
+// power of two; returns that power's inverse.  Heads at or past `heads` are zero.
+__device__ __forceinline__ float load_q(const TokArgs& a, int i, int head0, int heads, uint32_t (&qf)[8]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint4 x[2] = {};
+    if (g < heads) {
+        const uint4* src = reinterpret_cast<const uint4*>(a.Q + (long long)i * a.q_stride + (head0 + g) * 64 + 16 * t);
+        x[0] = __ldg(src);
+        x[1] = __ldg(src + 1);
+    }
+    const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = __vmaxu2(m, w[k] & 0x7fff7fffu);
+    m = max(m & 0xffffu, m >> 16);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    // largest exponent to 2^12; an infinite or NaN row stays so in fp16
+    int e = 12 - ((int)(m >> 7) - 127);
+    e = min(max(e, -120), 120);
+    const float f = __uint_as_float((uint32_t)(e + 127) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) qf[k] = pack_f16(bf16lo(w[k]) * f, bf16hi(w[k]) * f);
+    return inv;
+}
+
+// Raw scores of a page: c[mt][0], c[mt][1]: key row 16 mt + key_row(g), heads 2 t and 2 t + 1; c[mt][2], [3]: 8 rows on.
+__device__ __forceinline__ void page_scores(const uint8_t* sk, const uint32_t (&qf)[8], int g, int t, float (&c)[4][4]) {
+    const int r = key_row(g);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+        const uint4 lo = *reinterpret_cast<const uint4*>(sk + chunk_at(16 * mt + r, t));
+        const uint4 hi = *reinterpret_cast<const uint4*>(sk + chunk_at(16 * mt + 8 + r, t));
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+        c[mt][0] = c[mt][1] = c[mt][2] = c[mt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)wl[j]), e4m3x2_to_f16x2((uint16_t)wh[j]),
+                                    e4m3x2_to_f16x2((uint16_t)(wl[j] >> 16)), e4m3x2_to_f16x2((uint16_t)(wh[j] >> 16))};
+            mma_f16(c[mt], af, qf[2 * j], qf[2 * j + 1]);
+        }
+    }
+}
+
+// A segment: pages [page0, page1) of one row.
+struct Segment {
+    int i, kvh, head0, heads, pages, page0, page1, len, seq;
+    long long row;  // i * (H_kv * groups) + its place among the token's rows
+};
+
+__device__ __forceinline__ Segment segment_at(const TokArgs& a, const int* pre, long long u, long long u1) {
+    const int R = a.c.Hkv * a.groups;
+    const long long pg = u / R;  // the row is the last with pre[i] <= pg and at least one page
+    int lo = 0, hi = a.n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= pg) lo = mid;
+        else hi = mid;
+    }
+    Segment s;
+    s.i = lo;
+    s.pages = pre[lo + 1] - pre[lo];
+    const long long rem = u - (long long)pre[lo] * R;
+    const int gr = (int)(rem / s.pages);
+    s.page0 = (int)(rem - (long long)gr * s.pages);
+    s.page1 = (int)min((long long)s.pages, s.page0 + (u1 - u));
+    s.row = (long long)lo * R + gr;
+    s.kvh = gr / a.groups;
+    const int grp = gr - s.kvh * a.groups;
+    s.head0 = s.kvh * a.G + grp * HG;
+    s.heads = min(HG, a.G - grp * HG);
+    s.seq = a.seqs[lo];
+    s.len = a.c.lens[s.seq];
+    return s;
+}
+
+// The pages of a segment, 32 at a time: lane j holds page base + j's number (-1: out of range) and scales.
+template <bool kV>
+struct PageRun {
+    int base, phys;
+    float ks, vs;
+    __device__ __forceinline__ void load(const TokArgs& a, const Segment& s, int b) {
+        const int p = b + (threadIdx.x & 31);
+        base = b;
+        phys = -1;
+        ks = vs = 0.f;
+        if (p < s.page1) {
+            phys = a.c.table[(size_t)s.seq * a.c.max_pages + p];
+            if (phys < 0 || phys >= a.c.n_pages) {
+                phys = -1;
+                cache_error(a.c);
+            } else {
+                const size_t blk = a.c.block(a.layer, phys, s.kvh);
+                ks = __ldg(a.c.ks + blk);
+                if (kV) vs = __ldg(a.c.vs + blk);
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------------------------------- softmax
+constexpr int S_STAGES = 3;
+constexpr int S_STAGE_BYTES = 2 * BLOCK_BYTES;
+struct PageMeta {
+    float ks, vs;
+    int valid;  // keys of the page that exist
+    int pad;
+};
+constexpr int S_RING = WARPS * S_STAGES * S_STAGE_BYTES;
+constexpr int S_META = S_RING;
+constexpr int S_PRE = S_META + WARPS * S_STAGES * (int)sizeof(PageMeta);
+constexpr int softmax_smem(int n) { return S_PRE + (n + 1) * 4; }
+
+// One page's share of O and of the sums.  kPart: the page holds fewer than 64 keys (rows behind the end may
+// hold anything).
+template <bool kPart>
+__device__ __forceinline__ void softmax_page(const uint8_t* sk, const uint8_t* sv, const PageMeta& meta,
+                                             const uint32_t (&qf)[8], float f0, float f1, int g, int t, float& m0, float& m1,
+                                             float& l0, float& l1, float (&o)[4][4]) {
+    float c[4][4];
+    page_scores(sk, qf, g, t, c);
+    const int r = key_row(g);
+    f0 *= meta.ks;
+    f1 *= meta.ks;
+    float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+        c[mt][0] *= f0;
+        c[mt][1] *= f1;
+        c[mt][2] *= f0;
+        c[mt][3] *= f1;
+        if (kPart) {
+            if (16 * mt + r >= meta.valid) c[mt][0] = c[mt][1] = -INFINITY;
+            if (16 * mt + 8 + r >= meta.valid) c[mt][2] = c[mt][3] = -INFINITY;
+        }
+        x0 = fmaxf(x0, fmaxf(c[mt][0], c[mt][2]));
+        x1 = fmaxf(x1, fmaxf(c[mt][1], c[mt][3]));
+    }
+#pragma unroll
+    for (int s = 4; s < 32; s <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, s));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, s));
+    }
+    if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
+        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+        const float s0 = n0 == m0 ? 1.f : exp2f(m0 - n0), s1 = n1 == m1 ? 1.f : exp2f(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= s0;
+        l1 *= s1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[i][0] *= s0;
+            o[i][1] *= s1;
+            o[i][2] *= s0;
+            o[i][3] *= s1;
+        }
+    }
+    // a head with no key yet (a page out of range alone) has m = -inf: any finite offset gives its weights 0
+    const float b0 = (m0 == -INFINITY ? 0.f : m0) - P_SHIFT, b1 = (m1 == -INFINITY ? 0.f : m1) - P_SHIFT;
+    float acc[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    const int ra = key_row(2 * t), rb = key_row(2 * t + 1);
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt) {
+        const float p0 = exp2f(c[mt][0] - b0), p1 = exp2f(c[mt][1] - b1);
+        const float p2 = exp2f(c[mt][2] - b0), p3 = exp2f(c[mt][3] - b1);
+        l0 += p0 + p2;
+        l1 += p1 + p3;
+        const uint32_t h0 = pack_f16(p0, p1), h1 = pack_f16(p2, p3);
+        const uint32_t pb0 = transpose8x8(h0), pb1 = transpose8x8(h1);
+        const float2 e0 = unpack_f16(h0), e1 = unpack_f16(h1);
+        const uint32_t pr0 = transpose8x8(pack_f16(p0 - e0.x, p1 - e0.y)), pr1 = transpose8x8(pack_f16(p2 - e1.x, p3 - e1.y));
+        uint2 va = *reinterpret_cast<const uint2*>(sv + chunk_at(16 * mt + ra, g >> 1) + 8 * (g & 1));
+        uint2 vb = *reinterpret_cast<const uint2*>(sv + chunk_at(16 * mt + rb, g >> 1) + 8 * (g & 1));
+        uint2 vc = *reinterpret_cast<const uint2*>(sv + chunk_at(16 * mt + 8 + ra, g >> 1) + 8 * (g & 1));
+        uint2 vd = *reinterpret_cast<const uint2*>(sv + chunk_at(16 * mt + 8 + rb, g >> 1) + 8 * (g & 1));
+        if (kPart) {
+            if (16 * mt + ra >= meta.valid) va = make_uint2(0, 0);
+            if (16 * mt + rb >= meta.valid) vb = make_uint2(0, 0);
+            if (16 * mt + 8 + ra >= meta.valid) vc = make_uint2(0, 0);
+            if (16 * mt + 8 + rb >= meta.valid) vd = make_uint2(0, 0);
+        }
+        const uint32_t wa[2] = {va.x, va.y}, wb[2] = {vb.x, vb.y}, wc[2] = {vc.x, vc.y}, wd[2] = {vd.x, vd.y};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // dimensions 8 g + 2 i (product row g) and 8 g + 2 i + 1 (row g + 8)
+            const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+            const uint32_t u = __byte_perm(wa[i >> 1], wb[i >> 1], sel), v = __byte_perm(wc[i >> 1], wd[i >> 1], sel);
+            const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)u), e4m3x2_to_f16x2((uint16_t)(u >> 16)),
+                                    e4m3x2_to_f16x2((uint16_t)v), e4m3x2_to_f16x2((uint16_t)(v >> 16))};
+            mma_f16(acc[i], af, pb0, pb1);
+            mma_f16(acc[i], af, pr0, pr1);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][k] = fmaf(meta.vs, acc[i][k], o[i][k]);
+}
+
+// Eight consecutive output numbers of one head.
+__device__ __forceinline__ void store8(void* O, int f32, size_t at, const float (&v)[8]) {
+    if (f32) {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(O) + at);
+        d[0] = make_float4(v[0], v[1], v[2], v[3]);
+        d[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(O) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+__global__ void __launch_bounds__(WARPS * 32, 1) token_softmax_kernel(const TokArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    int* pre = reinterpret_cast<int*>(smem + S_PRE);
+    page_prefix(a, pre);
+    const Deal deal = deal_of(a, pre[a.n]);
+    const int w = warp * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
+    if (w >= deal.warps) return;
+    uint8_t* ring = smem + warp * S_STAGES * S_STAGE_BYTES;
+    PageMeta* metas = reinterpret_cast<PageMeta*>(smem + S_META) + warp * S_STAGES;
+    const uint32_t ring_u = smem_u32(ring);
+
+    const long long u0 = deal.start(w), u1 = deal.start(w + 1);
+    for (long long u = u0; u < u1;) {
+        const Segment s = segment_at(a, pre, u, u1);
+        uint32_t qf[8];
+        const float qinv = load_q(a, s.i, s.head0, s.heads, qf);
+        // x = S log2 e = raw * f for the lane's two heads
+        const float f0 = a.scale * LOG2E_F * __shfl_sync(0xffffffffu, qinv, 8 * t);
+        const float f1 = a.scale * LOG2E_F * __shfl_sync(0xffffffffu, qinv, 8 * t + 4);
+        PageRun<true> run;
+        run.load(a, s, s.page0);
+        auto fetch = [&](int p) {  // page p of the segment into its stage
+            if (p < s.page1) {
+                if (p >= run.base + 32) run.load(a, s, p);
+                const int phys = __shfl_sync(0xffffffffu, run.phys, p - run.base);
+                const float ks = __shfl_sync(0xffffffffu, run.ks, p - run.base);
+                const float vs = __shfl_sync(0xffffffffu, run.vs, p - run.base);
+                const int st = (p - s.page0) % S_STAGES;
+                if (lane == 0) metas[st] = PageMeta{ks, vs, phys < 0 ? 0 : min(PAGE, s.len - p * PAGE), 0};
+                if (phys >= 0) {
+                    const size_t blk = a.c.block(a.layer, phys, s.kvh) * BLOCK_BYTES;
+                    load_block(ring_u + st * S_STAGE_BYTES, a.c.K + blk, lane);
+                    load_block(ring_u + st * S_STAGE_BYTES + BLOCK_BYTES, a.c.V + blk, lane);
+                }
+            }
+            cp_commit();
+        };
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, o[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+        for (int k = 0; k < S_STAGES - 1; ++k) fetch(s.page0 + k);
+        for (int p = s.page0; p < s.page1; ++p) {
+            fetch(p + S_STAGES - 1);
+            cp_wait<S_STAGES - 1>();
+            __syncwarp();
+            const int st = (p - s.page0) % S_STAGES;
+            const uint8_t* sk = ring + st * S_STAGE_BYTES;
+            const PageMeta meta = metas[st];
+            if (meta.valid == PAGE) softmax_page<false>(sk, sk + BLOCK_BYTES, meta, qf, f0, f1, g, t, m0, m1, l0, l1, o);
+            else softmax_page<true>(sk, sk + BLOCK_BYTES, meta, qf, f0, f1, g, t, m0, m1, l0, l1, o);
+            __syncwarp();  // the stage may be filled again
+        }
+#pragma unroll
+        for (int k = 4; k < 32; k <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, k);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, k);
+        }
+        // the lane's heads 2 t, 2 t + 1, dimensions 8 g .. 8 g + 7
+        const float v0[8] = {o[0][0], o[0][2], o[1][0], o[1][2], o[2][0], o[2][2], o[3][0], o[3][2]};
+        const float v1[8] = {o[0][1], o[0][3], o[1][1], o[1][3], o[2][1], o[2][3], o[3][1], o[3][3]};
+        const bool whole = s.page0 == 0 && s.page1 == s.pages;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int h = 2 * t + k;
+            const float m = k ? m1 : m0, l = k ? l1 : l0;
+            if (h >= s.heads) continue;
+            if (whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;  // no key: every page out of range
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = (k ? v1[j] : v0[j]) * inv;
+                const size_t row = (size_t)s.i * a.H + s.head0 + h;
+                store8(a.O, a.out_f32, row * 64 + 8 * g, v);
+                if (g == 0) a.tau[row] = l == 0.f ? INFINITY : (m - P_SHIFT + log2f(l)) * LN2_F;
+            } else {
+                const size_t slot = ((size_t)w * 2 + (u == u0 ? 0 : 1)) * HG + h;
+                float4* d = reinterpret_cast<float4*>(a.part_o + slot * 64 + 8 * g);
+                const float* v = k ? v1 : v0;
+                d[0] = make_float4(v[0], v[1], v[2], v[3]);
+                d[1] = make_float4(v[4], v[5], v[6], v[7]);
+                if (g == 0) a.part_ml[slot] = make_float2(m, l);
+            }
+        }
+        u += s.page1 - s.page0;
+    }
+}
+
+// Where a row's segments lie: warps w0 .. w1, the first in slot s0 of its warp, the others in slot 0.
+struct RowParts {
+    int w0, w1, s0;
+    __device__ __forceinline__ size_t slot(int k, int h) const { return ((size_t)(w0 + k) * 2 + (k == 0 ? s0 : 0)) * HG + h; }
+};
+__device__ __forceinline__ RowParts row_parts(const TokArgs& a, const Deal& d, int first_page, int pages, int kvh, int grp) {
+    const long long u = (long long)first_page * a.c.Hkv * a.groups + (long long)(kvh * a.groups + grp) * pages;
+    RowParts r;
+    r.w0 = d.owner(u);
+    r.w1 = d.owner(u + pages - 1);
+    r.s0 = d.start(r.w0) == u ? 0 : 1;
+    return r;
+}
+
+constexpr int JT = 128;  // threads of the joining kernels, one CTA per (token, query head)
+
+// Joins a row's segments: O = sum_k 2^(m_k - m) o_k / sum_k 2^(m_k - m) l_k.  Four warps take the segments in
+// turn, a lane two dimensions; the warps' sums are added in order.
+__global__ void __launch_bounds__(JT) token_softmax_join_kernel(const TokArgs a) {
+    __shared__ float2 acc[4][32];
+    __shared__ float sums[4];
+    __shared__ float maxs[4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int i = blockIdx.x / a.H, head = blockIdx.x - i * a.H;
+    const int first = a.prefix[i], pages = a.prefix[i + 1] - first;
+    const size_t row = (size_t)i * a.H + head;
+    if (pages == 0) {  // an empty sequence
+        if (tid < 8) {
+            const float z[8] = {};
+            store8(a.O, a.out_f32, row * 64 + 8 * tid, z);
+        }
+        if (tid == 0) a.tau[row] = INFINITY;
+        return;
+    }
+    const Deal d = deal_of(a, a.prefix[a.n]);
+    const int kvh = head / a.G, in = head - kvh * a.G, grp = in / HG, h = in - grp * HG;
+    const RowParts r = row_parts(a, d, first, pages, kvh, grp);
+    const int n = r.w1 - r.w0 + 1;
+    if (n == 1) return;  // finished by its warp
+    float m = -INFINITY;
+    for (int k = tid; k < n; k += JT) m = fmaxf(m, a.part_ml[r.slot(k, h)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) maxs[warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(maxs[0], maxs[1]), fmaxf(maxs[2], maxs[3]));
+    const float base = m == -INFINITY ? 0.f : m;
+    float2 v = make_float2(0.f, 0.f);
+    float l = 0.f;
+#pragma unroll 4
+    for (int k = warp; k < n; k += 4) {
+        const size_t s = r.slot(k, h);
+        const float2 ml = a.part_ml[s];
+        const float2 x = reinterpret_cast<const float2*>(a.part_o + s * 64)[lane];
+        const float f = exp2f(ml.x - base);
+        l = fmaf(f, ml.y, l);
+        v.x = fmaf(f, x.x, v.x);
+        v.y = fmaf(f, x.y, v.y);
+    }
+    acc[warp][lane] = v;
+    if (lane == 0) sums[warp] = l;
+    __syncthreads();
+    if (warp == 0) {
+        l = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        v.x = ((acc[0][lane].x + acc[1][lane].x) + (acc[2][lane].x + acc[3][lane].x)) * inv;
+        v.y = ((acc[0][lane].y + acc[1][lane].y) + (acc[2][lane].y + acc[3][lane].y)) * inv;
+        if (a.out_f32) reinterpret_cast<float2*>(static_cast<float*>(a.O) + row * 64)[lane] = v;
+        else reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.O) + row * 64)[lane] = __floats2bfloat162_rn(v.x, v.y);
+        if (lane == 0) a.tau[row] = l == 0.f ? INFINITY : (m - P_SHIFT + log2f(l)) * LN2_F;
+    }
+}
+
+// ------------------------------------------------------------------------------------- 1.5-entmax
+// The threshold of any part of a row is a lower bound of the row's, so a warp keeps from its segment only
+// the scores above the best bound it knows (about its own support: a few dozen of thousands), as lists in
+// shared memory, one per lane and head.  Lists that fill up are cut again at the threshold of all that
+// they hold.  What is left of a segment, at most GC entries per head, goes to the joining kernel, which
+// takes the best bound of all segments, solves for tau on the entries above it and reads the values of the
+// support.  Rows whose support is too large for a list (flat scores) are flagged; the joining kernel then
+// computes all their scores again from the cache, each time it needs them.
+constexpr int E_STAGES = 4;
+constexpr int LCAP = 20;   // entries per lane and head
+constexpr int E_RING = WARPS * E_STAGES * BLOCK_BYTES;
+constexpr int E_LIST = E_RING;                                  // float2 [2][LCAP][32] per warp
+constexpr int E_LIST_BYTES = 2 * LCAP * 32 * 8;
+constexpr int E_META = E_LIST + WARPS * E_LIST_BYTES;
+constexpr int E_PRE = E_META + WARPS * E_STAGES * 8;
+constexpr int entmax_smem(int n) { return E_PRE + (n + 1) * 4; }
+
+// Sum over the eight lanes that hold one head.
+__device__ __forceinline__ float sum_g(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    v += __shfl_xor_sync(0xffffffffu, v, 16);
+    return v;
+}
+__device__ __forceinline__ float max_g(float v) {
+    v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 16));
+    return v;
+}
+// A Newton step on sum max(0, s - t)^2 = 4 given its sums: convex and decreasing, so from a lower bound the
+// iterates rise and stay lower bounds.
+__device__ __forceinline__ float newton(float t, float s1, float s2) { return s1 > 0.f ? t + fmaxf(s2 - 4.f, 0.f) / (2.f * s1) : t; }
+// A bound less what rounding may have added to it.
+__device__ __forceinline__ float safe(float t) { return t - 2e-6f * fmaxf(1.f, fabsf(t)); }
+
+// Raises the cuts of the lane's two heads by `steps` Newton steps on all that the lists hold and drops what
+// lies below.  Warp-collective.
+__device__ __forceinline__ void prune(float2* list, int lane, int steps, float& cut0, float& cut1, int& n0, int& n1) {
+    const int most = __reduce_max_sync(0xffffffffu, max(n0, n1));
+    float t0 = cut0, t1 = cut1;
+    for (int it = 0; it < steps; ++it) {
+        float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
+        for (int e = 0; e < most; ++e) {
+            const float d = e < n0 ? fmaxf(list[e * 32 + lane].x - t0, 0.f) : 0.f;
+            const float f = e < n1 ? fmaxf(list[(LCAP + e) * 32 + lane].x - t1, 0.f) : 0.f;
+            a1 += d;
+            a2 = fmaf(d, d, a2);
+            b1 += f;
+            b2 = fmaf(f, f, b2);
+        }
+        t0 = newton(t0, sum_g(a1), sum_g(a2));
+        t1 = newton(t1, sum_g(b1), sum_g(b2));
+    }
+    cut0 = fmaxf(cut0, safe(t0));
+    cut1 = fmaxf(cut1, safe(t1));
+    int k0 = 0, k1 = 0;
+    for (int e = 0; e < most; ++e) {
+        if (e < n0) {
+            const float2 x = list[e * 32 + lane];
+            if (x.x > cut0) list[k0++ * 32 + lane] = x;
+        }
+        if (e < n1) {
+            const float2 x = list[(LCAP + e) * 32 + lane];
+            if (x.x > cut1) list[(LCAP + k1++) * 32 + lane] = x;
+        }
+    }
+    n0 = k0;
+    n1 = k1;
+}
+
+__global__ void __launch_bounds__(WARPS * 32, 1) token_entmax_kernel(const TokArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    int* pre = reinterpret_cast<int*>(smem + E_PRE);
+    page_prefix(a, pre);
+    const Deal deal = deal_of(a, pre[a.n]);
+    const int w = warp * gridDim.x + blockIdx.x;
+    if (w >= deal.warps) return;
+    uint8_t* ring = smem + warp * E_STAGES * BLOCK_BYTES;
+    float2* list = reinterpret_cast<float2*>(smem + E_LIST + warp * E_LIST_BYTES);
+    float2* metas = reinterpret_cast<float2*>(smem + E_META) + warp * E_STAGES;  // scale, keys
+    const uint32_t ring_u = smem_u32(ring);
+    const int r = key_row(g);
+
+    const long long u0 = deal.start(w), u1 = deal.start(w + 1);
+    for (long long u = u0; u < u1;) {
+        const Segment s = segment_at(a, pre, u, u1);
+        uint32_t qf[8];
+        const float qinv = load_q(a, s.i, s.head0, s.heads, qf);
+        const float f0 = a.scale * __shfl_sync(0xffffffffu, qinv, 8 * t);
+        const float f1 = a.scale * __shfl_sync(0xffffffffu, qinv, 8 * t + 4);
+        PageRun<false> run;
+        run.load(a, s, s.page0);
+        auto fetch = [&](int p) {
+            if (p < s.page1) {
+                if (p >= run.base + 32) run.load(a, s, p);
+                const int phys = __shfl_sync(0xffffffffu, run.phys, p - run.base);
+                const float ks = __shfl_sync(0xffffffffu, run.ks, p - run.base);
+                const int st = (p - s.page0) % E_STAGES;
+                if (lane == 0) metas[st] = make_float2(ks, __int_as_float(phys < 0 ? 0 : min(PAGE, s.len - p * PAGE)));
+                if (phys >= 0) load_block(ring_u + st * BLOCK_BYTES, a.c.K + a.c.block(a.layer, phys, s.kvh) * BLOCK_BYTES, lane);
+            }
+            cp_commit();
+        };
+        // a head that the group does not have takes nothing
+        const bool use0 = 2 * t < s.heads, use1 = 2 * t + 1 < s.heads;
+        float cut0 = use0 ? -INFINITY : INFINITY, cut1 = use1 ? -INFINITY : INFINITY;
+        int n0 = 0, n1 = 0;
+        bool odd0 = false, odd1 = false, over0 = false, over1 = false;  // not finite; lists too small
+#pragma unroll
+        for (int k = 0; k < E_STAGES - 1; ++k) fetch(s.page0 + k);
+        for (int p = s.page0; p < s.page1; ++p) {
+            fetch(p + E_STAGES - 1);
+            cp_wait<E_STAGES - 1>();
+            __syncwarp();
+            const int st = (p - s.page0) % E_STAGES;
+            float c[4][4];
+            const float2 meta = metas[st];
+            page_scores(ring + st * BLOCK_BYTES, qf, g, t, c);
+            __syncwarp();
+            const int valid = __float_as_int(meta.y);
+            float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt) {
+                c[mt][0] *= f0 * meta.x;
+                c[mt][1] *= f1 * meta.x;
+                c[mt][2] *= f0 * meta.x;
+                c[mt][3] *= f1 * meta.x;
+                if (valid < PAGE) {
+                    if (16 * mt + r >= valid) c[mt][0] = c[mt][1] = -INFINITY;
+                    if (16 * mt + 8 + r >= valid) c[mt][2] = c[mt][3] = -INFINITY;
+                }
+                x0 = max_nan(x0, max_nan(c[mt][0], c[mt][2]));
+                x1 = max_nan(x1, max_nan(c[mt][1], c[mt][3]));
+            }
+            // anything above the cuts? (a NaN compares as yes)
+            if (!__any_sync(0xffffffffu, !(x0 <= cut0) || !(x1 <= cut1))) continue;
+            x0 = max_g(x0);
+            x1 = max_g(x1);
+            odd0 |= valid > 0 && !(fabsf(x0) < INFINITY);
+            odd1 |= valid > 0 && !(fabsf(x1) < INFINITY);
+            if (p == s.page0 && valid > 0) {
+                // the first page's own threshold, from its largest score less two
+                float t0 = x0 - 2.f, t1 = x1 - 2.f;
+                for (int it = 0; it < 4; ++it) {
+                    float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
+#pragma unroll
+                    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                        for (int q = 0; q < 4; q += 2) {
+                            const float d = fmaxf(c[mt][q] - t0, 0.f), e = fmaxf(c[mt][q + 1] - t1, 0.f);
+                            a1 += d;
+                            a2 = fmaf(d, d, a2);
+                            b1 += e;
+                            b2 = fmaf(e, e, b2);
+                        }
+                    t0 = newton(t0, sum_g(a1), sum_g(a2));
+                    t1 = newton(t1, sum_g(b1), sum_g(b2));
+                }
+                cut0 = fmaxf(cut0, safe(t0));
+                cut1 = fmaxf(cut1, safe(t1));
+            }
+            cut0 = fmaxf(cut0, safe(x0 - 2.f));
+            cut1 = fmaxf(cut1, safe(x1 - 2.f));
+            const int key0 = p * PAGE + r;
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int q = 0; q < 4; q += 2) {
+                    const int key = key0 + 16 * mt + 4 * q;
+                    if (c[mt][q] > cut0) list[n0++ * 32 + lane] = make_float2(c[mt][q], __int_as_float(key));
+                    if (c[mt][q + 1] > cut1) list[(LCAP + n1++) * 32 + lane] = make_float2(c[mt][q + 1], __int_as_float(key));
+                }
+            if (__any_sync(0xffffffffu, max(n0, n1) > LCAP - 8)) {
+                prune(list, lane, 4, cut0, cut1, n0, n1);
+                // still no room for the next page: give the head up
+                over0 |= __any_sync(0xffffffffu, n0 > LCAP - 8) && sum_g(n0 > LCAP - 8 ? 1.f : 0.f) > 0.f;
+                over1 |= __any_sync(0xffffffffu, n1 > LCAP - 8) && sum_g(n1 > LCAP - 8 ? 1.f : 0.f) > 0.f;
+                if (over0) n0 = 0;
+                if (over1) n1 = 0;
+            }
+        }
+        prune(list, lane, 6, cut0, cut1, n0, n1);
+        // the heads' entries, lanes in order
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int n = k ? n1 : n0;
+            int x = n;
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            const int total = __shfl_sync(0xffffffffu, x, 28 + t);
+            const bool odd = k ? odd1 : odd0, over = (k ? over1 : over0) || total > GC;
+            const int h = 2 * t + k;
+            if (h >= s.heads) continue;
+            const size_t slot = (size_t)(w + s.row) * a.heads + h;
+            if (g == 0) {
+                a.cand_n[slot] = odd ? -2 : over ? -1 : total;
+                a.cand_cut[slot] = k ? cut1 : cut0;
+            }
+            if (!odd && !over)
+                for (int e = 0; e < n; ++e) a.cand[slot * GC + x - n + e] = list[(k * LCAP + e) * 32 + lane];
+        }
+        __syncwarp();  // the lists and stages are the next segment's
+        u += s.page1 - s.page0;
+    }
+}
+
+constexpr int JCAP = 2048;  // entries above the joint bound that the joining kernel holds, a quarter per warp
+
+__device__ __forceinline__ float4 block_sum4(float4 v, float4* part) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+    }
+    __syncthreads();
+    if (lane == 0) part[warp] = v;
+    __syncthreads();
+    const float4 a = part[0], b = part[1], c = part[2], d = part[3];
+    return make_float4((a.x + b.x) + (c.x + d.x), (a.y + b.y) + (c.y + d.y), (a.z + b.z) + (c.z + d.z), (a.w + b.w) + (c.w + d.w));
+}
+
+__device__ __forceinline__ float4 e4m3x4_to_f32(uint32_t v) {
+    const uint32_t lo = e4m3x2_to_f16x2((uint16_t)v), hi = e4m3x2_to_f16x2((uint16_t)(v >> 16));
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return make_float4(a.x, a.y, b.x, b.y);
+}
+
+// One CTA per (token, query head).
+__global__ void __launch_bounds__(JT) token_entmax_join_kernel(const TokArgs a) {
+    __shared__ float2 ent[JCAP];
+    __shared__ float4 part[4];
+    __shared__ float qs[64];
+    __shared__ float red[4];
+    __shared__ int counts[4];
+    __shared__ float4 osum[8][16];
+    __shared__ short seg_n[GRID * WARPS];
+    __shared__ float wts[JT];
+    __shared__ const uint8_t* vat[JT];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int i = blockIdx.x / a.H, head = blockIdx.x - i * a.H;
+    const int first = a.prefix[i], pages = a.prefix[i + 1] - first;
+    const size_t row = (size_t)i * a.H + head;
+    auto put = [&](float fill, float tau) {  // a row without weights
+        if (tid < 8) {
+            const float z[8] = {fill, fill, fill, fill, fill, fill, fill, fill};
+            store8(a.O, a.out_f32, row * 64 + 8 * tid, z);
+        }
+        if (tid == 0) a.tau[row] = tau;
+    };
+    if (pages == 0) {
+        put(0.f, INFINITY);
+        return;
+    }
+    const Deal d = deal_of(a, a.prefix[a.n]);
+    const int kvh = head / a.G, in = head - kvh * a.G, grp = in / HG, h = in - grp * HG;
+    const RowParts r = row_parts(a, d, first, pages, kvh, grp);
+    const int segs = r.w1 - r.w0 + 1;
+    const int seq = a.seqs[i], len = a.c.lens[seq];
+    const int* table = a.c.table + (size_t)seq * a.c.max_pages;
+    if (tid < 64) qs[tid] = __bfloat162float(a.Q[(long long)i * a.q_stride + head * 64 + tid]) * a.scale;
+
+    // the best bound of all segments, and whether the lists are whole
+    const size_t slot0 = ((size_t)r.w0 + ((size_t)i * a.c.Hkv + kvh) * a.groups + grp) * a.heads + h;  // then one slot per warp
+    float cut = -INFINITY;
+    int least = 0;
+    for (int k = tid; k < segs; k += JT) {
+        const int m = a.cand_n[slot0 + (size_t)k * a.heads];
+        seg_n[k] = (short)m;
+        least = min(least, m);
+        cut = fmaxf(cut, a.cand_cut[slot0 + (size_t)k * a.heads]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) cut = fmaxf(cut, __shfl_xor_sync(0xffffffffu, cut, o));
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (lane == 0) {
+        red[warp] = cut;
+        counts[warp] = least;
+    }
+    __syncthreads();
+    cut = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+    least = min(min(counts[0], counts[1]), min(counts[2], counts[3]));
+    __syncthreads();
+    if (least == -2) {
+        put(NAN, NAN);
+        return;
+    }
+    if (cut == -INFINITY && least == 0) {  // every page out of range
+        put(0.f, INFINITY);
+        return;
+    }
+    // entries above the bound: each warp takes every fourth segment, in order, into its quarter of the list
+    bool listed = least == 0;
+    if (listed) {
+        float2* mine = ent + warp * (JCAP / 4);
+        int at = 0;
+        for (int k0 = warp; k0 < segs; k0 += 16) {
+            float2 x[4];
+            int n[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {  // four segments' first entries in flight
+                const int k = k0 + 4 * q;
+                n[q] = k < segs ? seg_n[k] : 0;
+                x[q] = make_float2(-INFINITY, 0.f);
+                if (lane < n[q]) x[q] = a.cand[(slot0 + (size_t)k * a.heads) * GC + lane];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + 4 * q;
+                for (int e = lane;;) {
+                    const uint32_t keep = __ballot_sync(0xffffffffu, x[q].x > cut);
+                    const int to = at + __popc(keep & ((1u << lane) - 1u));
+                    if (x[q].x > cut && to < JCAP / 4) mine[to] = x[q];
+                    at += __popc(keep);
+                    e += 32;
+                    if (e - lane >= n[q]) break;
+                    x[q] = make_float2(-INFINITY, 0.f);
+                    if (e < n[q]) x[q] = a.cand[(slot0 + (size_t)k * a.heads) * GC + e];
+                }
+            }
+        }
+        if (lane == 0) counts[warp] = at;
+    }
+    __syncthreads();
+    int total = 0;
+    if (listed) {
+        listed = max(max(counts[0], counts[1]), max(counts[2], counts[3])) <= JCAP / 4;
+        total = counts[0] + counts[1] + counts[2] + counts[3];
+    }
+    const int b1 = counts[0], b2 = b1 + counts[1], b3 = b2 + counts[2];
+    auto place = [&](int j) {  // entry j of the four quarters behind each other
+        return j < b1 ? j : j < b2 ? JCAP / 4 + j - b1 : j < b3 ? JCAP / 2 + j - b2 : 3 * (JCAP / 4) + j - b3;
+    };
+
+    // the score of key j again from the cache; -inf for a page out of range
+    auto score = [&](int j) -> float {
+        const int phys = table[j / PAGE];
+        if (phys < 0 || phys >= a.c.n_pages) return -INFINITY;
+        const size_t blk = a.c.block(a.layer, phys, kvh);
+        const uint4* src = reinterpret_cast<const uint4*>(a.c.K + blk * BLOCK_BYTES + (j % PAGE) * 64);
+        float acc = 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint4 x = __ldg(src + q);
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float4 y = e4m3x4_to_f32(v[e]);
+                const float* qq = qs + 16 * q + 4 * e;
+                acc = fmaf(qq[0], y.x, fmaf(qq[1], y.y, fmaf(qq[2], y.z, fmaf(qq[3], y.w, acc))));
+            }
+        }
+        return acc * a.c.ks[blk];
+    };
+    const int count = listed ? total : len;
+    // Newton's method from the bound until it stops rising, then the closed form on the support it leaves:
+    // tau = mean - sqrt(4 / k - variance) of the k scores above
+    float t = cut;
+    if (!listed) {
+        // bounds of flagged segments may be far below: start at the row's largest score less two
+        float m = -INFINITY;
+        for (int j = tid; j < len; j += JT) m = max_nan(m, score(j));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (lane == 0) red[warp] = m;
+        __syncthreads();
+        m = max_nan(max_nan(red[0], red[1]), max_nan(red[2], red[3]));
+        if (!(fabsf(m) < INFINITY)) {
+            put(NAN, NAN);
+            return;
+        }
+        t = fmaxf(t, safe(m - 2.f));
+    }
+    for (int it = 0; it < 24; ++it) {
+        float s1 = 0.f, s2 = 0.f;
+        for (int j = tid; j < count; j += JT) {
+            const float x = fmaxf((listed ? ent[place(j)].x : score(j)) - t, 0.f);
+            s1 += x;
+            s2 = fmaf(x, x, s2);
+        }
+        const float4 s = block_sum4(make_float4(s1, s2, 0.f, 0.f), part);
+        const float next = newton(t, s.x, s.y);
+        const bool done = next - t <= 1e-6f * fmaxf(1.f, fabsf(t));  // uniform
+        t = next;
+        if (done) break;
+    }
+    {
+        float k = 0.f, s1 = 0.f, s2 = 0.f;  // of x = s - t over the support
+        for (int j = tid; j < count; j += JT) {
+            const float x = (listed ? ent[place(j)].x : score(j)) - t;
+            if (x > 0.f) {
+                k += 1.f;
+                s1 += x;
+                s2 = fmaf(x, x, s2);
+            }
+        }
+        const float4 s = block_sum4(make_float4(k, s1, s2, 0.f), part);
+        if (s.x > 0.f) {
+            const float mean = s.y / s.x, var = fmaxf(s.z / s.x - mean * mean, 0.f);
+            const float fix = mean - sqrtf(fmaxf(4.f / s.x - var, 0.f));
+            if (fabsf(fix) <= 1e-5f * fmaxf(1.f, fabsf(t))) t += fix;
+        }
+    }
+    // O = sum p_j V_j.  Weights and places of up to JT keys at a time in shared memory, then eight groups of 16
+    // lanes, a key each, four dimensions a lane
+    const int grp16 = tid >> 4, l16 = tid & 15;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < count; j0 += JT) {
+        const int j = j0 + tid;
+        float w = 0.f;
+        const uint8_t* at = a.c.V;
+        if (j < count) {
+            float2 x = make_float2(0.f, __int_as_float(j));
+            if (listed) x = ent[place(j)];
+            else x.x = score(j);
+            const float d = x.x - t;
+            if (d > 0.f) {
+                const int key = __float_as_int(x.y);
+                const size_t blk = a.c.block(a.layer, table[key / PAGE], kvh);
+                w = 0.25f * d * d * a.c.vs[blk];
+                at += blk * BLOCK_BYTES + (key % PAGE) * 64;
+            }
+        }
+        // the keys of the support to the front, in order
+        const uint32_t keep = __ballot_sync(0xffffffffu, w != 0.f);
+        __syncthreads();  // the batch before is read
+        if (lane == 0) counts[warp] = __popc(keep);
+        __syncthreads();
+        int to = __popc(keep & ((1u << lane) - 1u));
+        for (int v = 0; v < warp; ++v) to += counts[v];
+        if (w != 0.f) {
+            wts[to] = w;
+            vat[to] = at;
+        }
+        const int m = counts[0] + counts[1] + counts[2] + counts[3];
+        __syncthreads();
+#pragma unroll 4
+        for (int e = grp16; e < m; e += 8) {
+            const float p = wts[e];
+            const float4 v = e4m3x4_to_f32(__ldg(reinterpret_cast<const uint32_t*>(vat[e]) + l16));
+            o.x = fmaf(p, v.x, o.x);
+            o.y = fmaf(p, v.y, o.y);
+            o.z = fmaf(p, v.z, o.z);
+            o.w = fmaf(p, v.w, o.w);
+        }
+    }
+    osum[grp16][l16] = o;
+    __syncthreads();
+    if (tid < 16) {
+        o = osum[0][tid];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            o.x += osum[k][tid].x;
+            o.y += osum[k][tid].y;
+            o.z += osum[k][tid].z;
+            o.w += osum[k][tid].w;
+        }
+        if (a.out_f32) {
+            reinterpret_cast<float4*>(static_cast<float*>(a.O) + row * 64)[tid] = o;
+        } else {
+            __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.O) + row * 64) + 2 * tid;
+            dst[0] = __floats2bfloat162_rn(o.x, o.y);
+            dst[1] = __floats2bfloat162_rn(o.z, o.w);
+        }
+        if (tid == 0) a.tau[row] = t;
+    }
+}
+
+size_t align256(size_t n) { return (n + 255) & ~size_t(255); }
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool is_softmax(float alpha) { return fabsf(alpha - 1.f) < 1e-4f; }
+
+size_t entmax_slots(int n, int H, int Hkv) {
+    const int G = H / Hkv, groups = (G + HG - 1) / HG;
+    return ((size_t)GRID * WARPS + (size_t)n * Hkv * groups) * std::min(G, HG);
+}
+size_t ws_bytes_of(int n, int H, int Hkv, float alpha) {
+    const bool soft = is_softmax(alpha);
+    const size_t slots = soft ? (size_t)GRID * WARPS * 2 * HG : entmax_slots(n, H, Hkv);
+    size_t b = align256(((size_t)n + 1) * 4);
+    if (soft) b += align256(slots * 64 * 4) + align256(slots * 8);
+    else b += 2 * align256(slots * 4) + align256(slots * GC * 8);
+    return b;
+}
+
+}  // namespace
+}  // namespace entmax
+
+using namespace entmax;
+
+extern "C" {
+
+size_t entmax_cache_attn_workspace_size(int n, int H, int H_kv, float alpha) {
+    return n <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 ? 0 : ws_bytes_of(n, H, H_kv, alpha);
+}
+
+int entmax_cache_attn(const entmax_cache* c, int layer, const void* Q, long long q_stride, const int32_t* seqs, int n,
+                      int max_len, float scale, float alpha, int H, void* O, int out_dtype, float* tau, void* workspace,
+                      size_t ws_bytes, cudaStream_t stream) {
+    if (!c || n < 0 || H < 0 || max_len < 0) return ENTMAX_ERR_ARG;
+    if (!(scale > 0.f) || !isfinite(scale)) return ENTMAX_ERR_ARG;
+    if (!is_softmax(alpha) && !(alpha > 1.f && alpha <= 2.f)) return ENTMAX_ERR_ARG;
+    if (!is_softmax(alpha) && alpha != 1.5f) return ENTMAX_ERR_UNSUPPORTED;
+    if (out_dtype != ENTMAX_BF16 && out_dtype != ENTMAX_F32) return ENTMAX_ERR_ARG;
+    if (layer < 0 || layer >= c->n_layers) return ENTMAX_ERR_ARG;
+    if (c->H_kv < 1 || H % c->H_kv != 0) return ENTMAX_ERR_ARG;
+    if (n > MAX_TOKENS) return ENTMAX_ERR_UNSUPPORTED;
+    if (n == 0 || H == 0) return ENTMAX_OK;
+    if (max_len > (long long)c->max_pages * PAGE) return ENTMAX_ERR_ARG;
+    if (!Q || !seqs || !O || !tau || !aligned(Q, 16) || !aligned(seqs, 4) || !aligned(O, 16) || !aligned(tau, 4))
+        return ENTMAX_ERR_ARG;
+    if (q_stride % 8 || q_stride < 64ll * H) return ENTMAX_ERR_ARG;
+    if ((long long)n * pages_of(max_len) > 0x7fffffffll || (long long)n * H > 0x7fffffffll) return ENTMAX_ERR_UNSUPPORTED;
+    if (!workspace || ws_bytes < ws_bytes_of(n, H, c->H_kv, alpha)) return ENTMAX_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return ENTMAX_ERR_ARG;
+    TokArgs a{};
+    int rc = cache_args(c, &a.c);
+    if (rc) return rc;
+    const bool soft = is_softmax(alpha);
+    a.Q = static_cast<const __nv_bfloat16*>(Q);
+    a.q_stride = q_stride;
+    a.seqs = seqs;
+    a.n = n;
+    a.H = H;
+    a.G = H / c->H_kv;
+    a.groups = (a.G + HG - 1) / HG;
+    a.layer = layer;
+    a.max_len = max_len;
+    a.scale = scale;
+    a.O = O;
+    a.out_f32 = out_dtype == ENTMAX_F32;
+    a.tau = tau;
+    a.warps = GRID * WARPS;
+    a.heads = std::min(a.G, HG);
+    const size_t slots = soft ? (size_t)a.warps * 2 * HG : entmax_slots(n, H, c->H_kv);
+    uint8_t* p = static_cast<uint8_t*>(workspace);
+    a.prefix = reinterpret_cast<int*>(p);
+    p += align256(((size_t)n + 1) * 4);
+    if (soft) {
+        a.part_o = reinterpret_cast<float*>(p);
+        p += align256(slots * 64 * 4);
+        a.part_ml = reinterpret_cast<float2*>(p);
+    } else {
+        a.cand_n = reinterpret_cast<int*>(p);
+        p += align256(slots * 4);
+        a.cand_cut = reinterpret_cast<float*>(p);
+        p += align256(slots * 4);
+        a.cand = reinterpret_cast<float2*>(p);
+    }
+    const void* f = soft ? reinterpret_cast<const void*>(token_softmax_kernel) : reinterpret_cast<const void*>(token_entmax_kernel);
+    rc = abi_record(ensure_smem_attr(f, soft ? softmax_smem(MAX_TOKENS) : entmax_smem(MAX_TOKENS), soft ? 17 : 18));
+    if (rc) return rc;
+    if (soft) token_softmax_kernel<<<GRID, WARPS * 32, softmax_smem(n), stream>>>(a);
+    else token_entmax_kernel<<<GRID, WARPS * 32, entmax_smem(n), stream>>>(a);
+    rc = abi_record(cudaGetLastError());
+    if (rc) return rc;
+    if (soft) token_softmax_join_kernel<<<n * H, JT, 0, stream>>>(a);
+    else token_entmax_join_kernel<<<n * H, JT, 0, stream>>>(a);
+    return abi_record(cudaGetLastError());
+}
+
+}  // extern "C"

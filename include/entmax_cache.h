@@ -102,6 +102,31 @@ ENTMAX_API int entmax_cache_append(const entmax_cache* c, int layer, const void*
                                    long long v_stride, const int32_t* seqs, const int32_t* cu, int n, int T,
                                    cudaStream_t stream);
 
+/*
+ * Attention of one token of each of n sequences over all of its sequence's tokens in one layer (the
+ * token's own key and value among them, if they were appended).
+ *   Q           bf16, token i's query head h at [i * q_stride + 64 h]; q_stride in elements, a multiple of 8, at
+ *               least 64 H; 16-byte aligned.
+ *   seqs        device int32 [n], row i's sequence; a sequence may be named several times.
+ *   max_len     no sequence of the list is longer (at most 64 max_pages).
+ *   alpha       1.5 (1.5-entmax) or within 1e-4 of 1 (softmax); other values in (1, 2] return
+ *               ENTMAX_ERR_UNSUPPORTED, any others ENTMAX_ERR_ARG.
+ *   H           query heads, a multiple of H_kv.
+ *   O           [n][H][64] bf16 or fp32 (out_dtype), 16-byte aligned; tau [n][H] fp32: the threshold, for softmax
+ *               log sum exp of the scores.  An empty sequence gives O = 0, tau = +inf; so does a row that is
+ *               left out (its sequence or length out of range).  Pages out of range are left out of their row.
+ *               Rows with NaN among their scores give NaN.
+ *   workspace   device buffer of entmax_cache_attn_workspace_size(n, H, H_kv, alpha) bytes, 256-byte
+ *               aligned, of the call's own while it runs.
+ * Numbers: products of the e4m3 keys and bf16 queries are exact and summed in fp32; softmax weights
+ * multiply the values as two fp16 parts (22 bits), 1.5-entmax weights in fp32.  Results are the
+ * same bit for bit from run to run.  n <= 4096.
+ */
+ENTMAX_API int entmax_cache_attn(const entmax_cache* c, int layer, const void* Q, long long q_stride,
+                                 const int32_t* seqs, int n, int max_len, float scale, float alpha, int H, void* O,
+                                 int out_dtype, float* tau, void* workspace, size_t ws_bytes, cudaStream_t stream);
+ENTMAX_API size_t entmax_cache_attn_workspace_size(int n, int H, int H_kv, float alpha);
+
 /* Synchronises `stream`, then returns and clears the cache status word of the current device: ENTMAX_OK,
  * or ENTMAX_ERR_ARG if a kernel left an entry out since the last read. */
 ENTMAX_API int entmax_cache_status(cudaStream_t stream);

@@ -63,6 +63,38 @@ def test_bad_arguments(name, kw, code):
     assert call(name, cache(), **kw) == code
 
 
+def attn(c, **kw):
+    a = dict(layer=0, Q=P, qs=64 * 6, seqs=P, n=2, max_len=320, scale=0.125, alpha=1.5, H=6, O=P, out=0, tau=P, ws=P, ws_bytes=1 << 40)
+    a.update(kw)
+    return E.lib.entmax_cache_attn(ctypes.addressof(c), a["layer"], a["Q"], a["qs"], a["seqs"], a["n"], a["max_len"], a["scale"],
+                                   a["alpha"], a["H"], a["O"], a["out"], a["tau"], a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), E.ENTMAX_ERR_ARG), (dict(n=4097), E.ENTMAX_ERR_UNSUPPORTED), (dict(n=0), E.ENTMAX_OK),
+    (dict(H=7), E.ENTMAX_ERR_ARG), (dict(H=-3), E.ENTMAX_ERR_ARG), (dict(layer=2), E.ENTMAX_ERR_ARG),
+    (dict(alpha=1.6), E.ENTMAX_ERR_UNSUPPORTED), (dict(alpha=0.9), E.ENTMAX_ERR_ARG), (dict(alpha=2.1), E.ENTMAX_ERR_ARG),
+    (dict(alpha=float("nan")), E.ENTMAX_ERR_ARG), (dict(scale=-1.0), E.ENTMAX_ERR_ARG), (dict(out=2), E.ENTMAX_ERR_ARG),
+    (dict(max_len=321), E.ENTMAX_ERR_ARG), (dict(max_len=-1), E.ENTMAX_ERR_ARG), (dict(Q=None), E.ENTMAX_ERR_ARG),
+    (dict(Q=P + 8), E.ENTMAX_ERR_ARG), (dict(qs=64 * 6 - 8), E.ENTMAX_ERR_ARG), (dict(qs=64 * 6 + 4), E.ENTMAX_ERR_ARG),
+    (dict(seqs=None), E.ENTMAX_ERR_ARG), (dict(O=P + 8), E.ENTMAX_ERR_ARG), (dict(tau=None), E.ENTMAX_ERR_ARG),
+    (dict(ws=None), E.ENTMAX_ERR_WORKSPACE), (dict(ws_bytes=1000), E.ENTMAX_ERR_WORKSPACE), (dict(ws=P + 16), E.ENTMAX_ERR_ARG),
+])
+def test_bad_attn_arguments(kw, code):
+    assert attn(cache(), **kw) == code
+
+
+@pytest.mark.parametrize("kw", [dict(K=None), dict(refs=P + 1), dict(n_seqs=0)])
+def test_attn_on_bad_caches(kw):
+    assert attn(cache(**kw)) == E.ENTMAX_ERR_ARG
+
+
+def test_attn_workspace_size():
+    size = E.lib.entmax_cache_attn_workspace_size
+    assert size(0, 4, 4, 1.5) == size(3, 5, 2, 1.5) == size(3, 4, 0, 1.0) == 0
+    assert 0 < size(1, 4, 4, 1.0) <= size(4096, 4, 4, 1.0) and size(1, 4, 4, 1.5) < size(64, 4, 4, 1.5) < size(64, 8, 4, 1.5)
+
+
 def test_workspace_size_grows_with_the_pool():
     small, large = cache(n_pages=8), cache(n_pages=100000)
     a, b = (E.lib.entmax_cache_workspace_size(ctypes.addressof(x)) for x in (small, large))

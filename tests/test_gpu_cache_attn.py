@@ -1,0 +1,309 @@
+"""Attention of single tokens over the 8-bit cache against fp64.
+
+Tolerances.  Keys, values and queries enter exactly.  Scores are sums of 64 exact products in fp32, scaled
+twice: |dS| <= delta = 2^-17 (1 + max|S|).
+  softmax:     a weight has the relative error 2 delta (exponent) + 2^-22 (two fp16 parts: each rounding is off by
+               half a step, 2^-11) + 2^-20 (exp2, sums), so |dO| <= (2 delta + 2^-22 + 2^-20) sum p |V| and |dtau| <=
+               delta + 2^-20 (1 + |tau|).  Weights below 2^-18 of the largest lose bits of the second part: at
+               most 2^-25 of a weight shifted by 2^15, 2^-40 each, N 2^-40 max|V| in all.
+  1.5-entmax:  tau moves by at most delta (it is 1-Lipschitz in the scores) plus its solver's 2^-18 (1 + |tau|);
+               p = (x/2)^2, so |dp| <= e (sqrt p + e) with e = delta + |dtau|; sums in fp32 add 2^-20.
+"""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from cache_model import VALUES
+
+pytestmark = pytest.mark.gpu
+PAGE = 64
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def make(lens, H_kv, n_layers=1, seed=0, spare=2, max_pages=None, n_pages=None, offset=0):
+    """A cache of random blocks holding sequences of the given lengths, in shuffled pages; everything that no
+    token names is NaN."""
+    import entmax_tcgen05_tma_b200 as E
+    rng = random.Random(seed)
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = sum((n + PAGE - 1) // PAGE for n in lens)
+    n_pages = n_pages or need + spare
+    max_pages = max_pages or max(1, max((n + PAGE - 1) // PAGE for n in lens))
+    shape = (n_layers, n_pages, H_kv)
+    pools = [torch.full(shape + (PAGE, 64), 0x7f, dtype=torch.uint8, device="cuda") for _ in "KV"]
+    scales = [torch.full(shape, float("nan"), device="cuda") for _ in "KV"]
+    table, refs = [[-1] * max_pages for _ in lens], [0] * n_pages
+    pages = list(range(offset, offset + need))
+    rng.shuffle(pages)
+    for s, n in enumerate(lens):
+        for k in range((n + PAGE - 1) // PAGE):
+            p = table[s][k] = pages.pop()
+            refs[p] = 1
+            rows = min(PAGE, n - k * PAGE)
+            for pool, scale in zip(pools, scales):
+                x = torch.randn((n_layers, H_kv, rows, 64), generator=g, device="cuda") * 80
+                pool[:, p, :, :rows] = x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+                scale[:, p] = torch.exp2(torch.randint(-8, -5, (n_layers, H_kv), generator=g, device="cuda").float())
+    return E.EntmaxCache(*(x.view(torch.float8_e4m3fn) for x in pools), *scales, ints(refs), ints(table), ints(lens))
+
+
+def tokens(c, layer, s):
+    """fp64 (K, V) [H_kv, len, 64] of a sequence."""
+    n = int(c.lens[s])
+    p = c.table[s, :(n + PAGE - 1) // PAGE].long()
+    out = []
+    for pool, scale in ((c.K, c.k_scale), (c.V, c.v_scale)):
+        x = VALUES[pool.view(torch.uint8)[layer, p].cpu().numpy()] * scale[layer, p].double().cpu().numpy()[..., None, None]
+        out.append(x.transpose(1, 0, 2, 3).reshape(x.shape[1], -1, 64)[:, :n])
+    return out
+
+
+def entmax_tau(S):
+    """1.5-entmax threshold of a row: on the k largest scores z, mean - sqrt(4/k - variance), for the largest k with
+    it below z_k."""
+    z = np.sort(S)[::-1] - S.max()
+    k = np.arange(1, z.size + 1)
+    mean = np.cumsum(z) / k
+    rest = 4.0 / k - (np.cumsum(z * z) / k - mean * mean)
+    root = mean - np.sqrt(np.maximum(rest, 0))
+    return S.max() + root[np.nonzero((rest >= 0) & (root < z))[0][-1]]
+
+
+def check(c, layer, Q, seqs, O, tau, scale, alpha):
+    q = Q.double().cpu().numpy()
+    O, tau = O.double().cpu().numpy(), tau.double().cpu().numpy()
+    G = Q.shape[1] // c.H_kv
+    for i, s in enumerate(seqs):
+        K, V = tokens(c, layer, s)
+        if K.shape[1] == 0:
+            assert (O[i] == 0).all() and (tau[i] == np.inf).all()
+            continue
+        for h in range(Q.shape[1]):
+            S = scale * (K[h // G] @ q[i, h])
+            delta = 2.0 ** -17 * (1 + np.abs(S).max())
+            if alpha == 1.0:
+                m = S.max()
+                ref = m + np.log(np.exp(S - m).sum())
+                p = np.exp(S - ref)
+                off, tol = 2 * delta + 2.0 ** -22 + 2.0 ** -20, delta + 2.0 ** -20 * (1 + abs(ref))
+                room = off * (p @ np.abs(V[h // G])) + S.size * 2.0 ** -40 * np.abs(V[h // G]).max()
+            else:
+                ref = entmax_tau(S)
+                p = np.maximum(0, (S - ref) / 2) ** 2
+                tol = delta + 2.0 ** -18 * (1 + abs(ref))
+                e = delta + tol
+                near = S > ref - 2 * e
+                room = ((e * (np.sqrt(p) + e) + 2.0 ** -20 * p) * near) @ np.abs(V[h // G])
+            assert abs(tau[i, h] - ref) <= tol, (i, h, tau[i, h], ref, tol)
+            err = np.abs(O[i, h] - p @ V[h // G])
+            assert (err <= room + 1e-30).all(), (i, h, err.max(), room.min())
+
+
+def run(c, layer, Q, seqs, alpha, scale=0.125, **kw):
+    import entmax_tcgen05_tma_b200 as E
+    kw.setdefault("max_len", c.max_pages * PAGE)
+    O, tau = E.entmax_cache_attn(c, layer, Q, ints(seqs), kw.pop("max_len"), scale=scale, alpha=alpha,
+                                 out_dtype=torch.float32, **kw)
+    Ob, taub = E.entmax_cache_attn(c, layer, Q, ints(seqs), c.max_pages * PAGE, scale=scale, alpha=alpha)
+    assert torch.equal(tau, taub) and torch.equal(O.to(torch.bfloat16), Ob)
+    return O, tau
+
+
+def queries(n, H, seed=0, strided=False):
+    g = torch.Generator(device="cuda").manual_seed(100 + seed)
+    q = torch.randn((n, H + (3 if strided else 0), 64), generator=g, device="cuda").to(torch.bfloat16)
+    return q[:, :H]
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+@pytest.mark.parametrize("H,H_kv", [(1, 1), (4, 4), (4, 1), (6, 2), (5, 1), (16, 2), (9, 1), (12, 1), (17, 1), (40, 2)])
+def test_lengths_and_head_groups(alpha, H, H_kv):
+    """Empty, one token, around the page's end, many pages; one head to three groups of query heads."""
+    lens = [0, 1, 63, 64, 65, 127, 200, 1000, 2, 3000]
+    c = make(lens, H_kv, n_layers=2, seed=H)
+    seqs = [9, 0, 1, 2, 3, 4, 5, 6, 7, 8, 7]  # out of order, one twice
+    Q = queries(len(seqs), H, H, strided=H % 2 == 1)
+    O, tau = run(c, 1, Q, seqs, alpha)
+    check(c, 1, Q, seqs, O, tau, 0.125, alpha)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+@pytest.mark.parametrize("n", [1, 2, 300])
+def test_few_long_and_many_short(alpha, n):
+    """One long context dealt to all warps, and more rows than warps."""
+    rng = random.Random(n)
+    lens = [20000] if n == 1 else [9000, 1] if n == 2 else [rng.randint(0, 400) for _ in range(n)]
+    c = make(lens, 8 if n == 300 else 2, seed=n)
+    Q = queries(n, 16 if n == 300 else 4, n)
+    seqs = list(range(n))
+    O, tau = run(c, 0, Q, seqs, alpha, max_len=max(lens))
+    check(c, 0, Q, seqs, O, tau, 0.125, alpha)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+@pytest.mark.parametrize("scale", [1e-4, 0.01, 1.0, 30.0])
+def test_flat_and_peaked_rows(alpha, scale):
+    """From supports that fill whole rows (1.5-entmax: the lists overflow) to single keys; zero queries among them."""
+    c = make([700, 5000, 64], 2, seed=5)
+    Q = queries(3, 6, 1).clone()
+    Q[0, 0] = 0
+    Q[1, 3:] = 0
+    O, tau = run(c, 0, Q, [0, 1, 2], alpha, scale)
+    check(c, 0, Q, [0, 1, 2], O, tau, scale, alpha)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_queries_of_all_magnitudes(alpha):
+    """Queries from 2^-100 to 2^20, and heads whose elements span 2^30."""
+    c = make([300], 1, seed=6)
+    Q = queries(1, 8, 2).float()
+    Q *= torch.exp2(torch.tensor([-100.0, -40, -10, 0, 3, 6, 0, 0], device="cuda"))[:, None]
+    Q[0, 6, ::2] *= 2.0 ** -30
+    Q[0, 7] = 0
+    Q[0, 7, 5] = 2.0 ** 4
+    Q = Q.to(torch.bfloat16)
+    O, tau = run(c, 0, Q, [0], alpha)
+    check(c, 0, Q, [0], O, tau, 0.125, alpha)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_not_finite(alpha):
+    """A NaN key makes the rows that read it NaN, a NaN value those that weigh it; others are untouched."""
+    import entmax_tcgen05_tma_b200 as E
+    c = make([200, 200, 200], 2, seed=7)
+    Q = queries(3, 4, 3)
+    clean = run(c, 0, Q, [0, 1, 2], alpha)
+    c.K.view(torch.uint8)[0, c.table[1, 2], 0, 3, 9] = 0x7f
+    O, tau = run_nan(c, Q, alpha)
+    assert torch.isnan(O[1, :2]).all() and torch.isnan(tau[1, :2]).all()
+    for a, b in zip((O, tau), clean):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[2], b[2]) and torch.equal(a[1, 2:], b[1, 2:])
+    if alpha == 1.0:
+        c.V.view(torch.uint8)[0, c.table[2, 0], 1, 3, 9] = 0xff
+        O, tau = run_nan(c, Q, alpha)
+        assert torch.isnan(O[2, 2:, 9]).all() and not torch.isnan(O[2, 2:, :9]).any() and torch.equal(tau[2], clean[1][2])
+    q = Q.clone()
+    q[0, 1, 5] = float("inf")
+    O, tau = run_nan(c, q, alpha)
+    assert torch.isnan(O[0, 1]).all() and torch.equal(O[0, 0], clean[0][0, 0])
+    assert E.entmax_cache_status() == 0
+
+
+def run_nan(c, Q, alpha):
+    import entmax_tcgen05_tma_b200 as E
+    return E.entmax_cache_attn(c, 0, Q, ints(list(range(Q.shape[0]))), c.max_pages * PAGE, alpha=alpha, out_dtype=torch.float32)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_rows_and_pages_out_of_range(alpha):
+    """Left out: sequences and lengths that do not exist give an empty row; a page that does not exist leaves its keys out."""
+    import entmax_tcgen05_tma_b200 as E
+    c = make([200, 300, 64, 100], 2, seed=8)
+    Q = queries(6, 4, 4)
+    c.lens[3] = c.max_pages * PAGE + 1
+    O, tau = run(c, 0, Q, [0, -1, 1, 4, 3, 2], alpha)
+    assert E.entmax_cache_status() == E.ENTMAX_ERR_ARG
+    for i in (1, 3, 4):
+        assert (O[i] == 0).all() and (tau[i] == float("inf")).all()
+    keep = [0, 2, 5]
+    check(c, 0, Q[keep], [0, 1, 2], O[keep], tau[keep], 0.125, alpha)
+    # longer than max_len says
+    O2, tau2 = E.entmax_cache_attn(c, 0, Q[:2], ints([0, 1]), 200, alpha=alpha, out_dtype=torch.float32)
+    assert torch.equal(O2[0], O[0]) and (O2[1] == 0).all() and E.entmax_cache_status() == E.ENTMAX_ERR_ARG
+    # a row whose page 1 is gone equals the row of its other pages; one whose only page is gone is empty
+    d = make([200, 300, 64, 100], 2, seed=8)
+    d.table[0, 1:3] = d.table[0, 2:4].clone()
+    d.lens[0] = 200 - 64
+    want = E.entmax_cache_attn(d, 0, Q[:1], ints([0]), 300, alpha=alpha, out_dtype=torch.float32)
+    for bad in (-1, c.n_pages, 1 << 30):
+        c.table[0, 1] = bad
+        c.table[2, 0] = bad
+        O, tau = E.entmax_cache_attn(c, 0, Q[:2], ints([0, 2]), 300, alpha=alpha, out_dtype=torch.float32)
+        assert E.entmax_cache_status() == E.ENTMAX_ERR_ARG
+        torch.testing.assert_close(O[0], want[0][0], rtol=1e-3, atol=1e-3)
+        torch.testing.assert_close(tau[0], want[1][0], rtol=1e-5, atol=1e-5)
+        assert (O[1] == 0).all() and (tau[1] == float("inf")).all()
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_same_bits_every_time_and_on_another_stream(alpha):
+    rng = random.Random(1)
+    lens = [rng.randint(1, 3000) for _ in range(12)]
+    c = make(lens, 4, seed=9)
+    Q = queries(12, 12, 5)
+    seqs = list(range(12))
+    a = run(c, 0, Q, seqs, alpha)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    import entmax_tcgen05_tma_b200 as E
+    with torch.cuda.stream(s):
+        b = E.entmax_cache_attn(c, 0, Q, ints(seqs), c.max_pages * PAGE, alpha=alpha, out_dtype=torch.float32)
+    ws = torch.full((E.entmax_cache_attn_workspace_size(12, 12, 4, alpha),), 0xff, dtype=torch.uint8, device="cuda")
+    d = E.entmax_cache_attn(c, 0, Q, ints(seqs), c.max_pages * PAGE, alpha=alpha, out_dtype=torch.float32, workspace=ws)
+    torch.cuda.synchronize()
+    for x in (b, d):
+        assert torch.equal(a[0], x[0]) and torch.equal(a[1], x[1])
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_two_graphs_follow_the_lengths(alpha):
+    """Two captured calls, replayed with lengths that change between replays."""
+    import entmax_tcgen05_tma_b200 as E
+    c = make([500, 64, 900], 2, seed=10, max_pages=15)
+    Q = [queries(3, 4, 6), queries(3, 4, 7)]
+    ids = ints([0, 1, 2])
+    O = [torch.zeros(3, 4, 64, device="cuda") for _ in Q]
+    tau = [torch.zeros(3, 4, device="cuda") for _ in Q]
+    E.entmax_cache_attn(c, 0, Q[0], ids, 960, alpha=alpha)
+    graphs = []
+    for k in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            E.entmax_cache_attn(c, 0, Q[k], ids, 960, alpha=alpha, out_dtype=torch.float32, O=O[k], tau=tau[k])
+        graphs.append(g)
+    for lens in ([500, 64, 900], [1, 0, 64], [450, 33, 899]):
+        c.lens.copy_(ints(lens))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for k in range(2):
+            check(c, 0, Q[k], [0, 1, 2], O[k], tau[k], 0.125, alpha)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_pools_past_four_gigabytes(alpha):
+    """Pages whose blocks lie past 2^32 bytes in each pool."""
+    n_pages = 140000
+    c = make([700, 90], 8, seed=11, n_pages=n_pages, offset=n_pages - 13)
+    assert int(c.table[0, 0]) * 8 * 4096 > 1 << 32
+    Q = queries(2, 8, 8)
+    O, tau = run(c, 0, Q, [0, 1], alpha)
+    check(c, 0, Q, [0, 1], O, tau, 0.125, alpha)
+
+
+def test_refusals():
+    import entmax_tcgen05_tma_b200 as E
+    c = make([64], 2)
+    q = queries(1, 4)
+    ids = ints([0])
+    for kw, code in ((dict(alpha=1.25), E.ENTMAX_ERR_UNSUPPORTED), (dict(alpha=2.5), E.ENTMAX_ERR_ARG),
+                     (dict(alpha=float("nan")), E.ENTMAX_ERR_ARG), (dict(scale=0.0), E.ENTMAX_ERR_ARG),
+                     (dict(max_len=65), E.ENTMAX_ERR_ARG), (dict(max_len=-1), E.ENTMAX_ERR_ARG), (dict(layer=1), E.ENTMAX_ERR_ARG)):
+        a = dict(layer=0, max_len=64)
+        a.update(kw)
+        with pytest.raises(E.EntmaxError) as e:
+            E.entmax_cache_attn(c, a.pop("layer"), q, ids, a.pop("max_len"), **a)
+        assert e.value.status == code
+    with pytest.raises(ValueError):
+        E.entmax_cache_attn(c, 0, queries(1, 3), ids, 64)
+    with pytest.raises(TypeError):
+        E.entmax_cache_attn(c, 0, q.float(), ids, 64)
+    with pytest.raises(ValueError):
+        E.entmax_cache_attn(c, 0, q, ints([0, 0]), 64)
+    O, tau = E.entmax_cache_attn(c, 0, queries(0, 4), ints([]), 64)
+    assert O.shape == (0, 4, 64) and tau.shape == (0, 4)
