@@ -48,6 +48,7 @@ from ._binding import (  # noqa: F401
 from ._serving import (  # noqa: F401
     ENTMAX_PAGE_TOKENS,
     EntmaxCache,
+    entmax_attn_prompt,
     entmax_cache_append,
     entmax_cache_attn,
     entmax_cache_attn_workspace_size,

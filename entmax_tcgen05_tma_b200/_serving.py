@@ -261,3 +261,38 @@ def entmax_cache_attn(cache, layer, Q, seqs, max_len, scale=None, alpha=1.5, out
                                      tau.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
                                      _handle(stream, c.device)), "entmax_cache_attn")
     return O, tau
+
+
+def entmax_attn_prompt(Q, K, V, cu, max_len, scale=None, alpha=1.5, out_dtype=torch.bfloat16, O=None, tau=None,
+                       stream=None):
+    """Causal attention over packed sequences of different lengths, with grouped heads.
+
+    Q: bf16 [T, H, 64]; K, V: bf16 [T, H_kv, 64], H % H_kv == 0; a token stride that is a multiple of 64
+    elements is allowed (slices of a fused projection).  cu: int32 device tensor [n + 1], sequence i has the
+    tokens cu[i] .. cu[i + 1] - 1; max_len: no sequence is longer.  alpha as in entmax_attn_fwd_ex.
+    Returns (O, tau): O [T, H, 64] in ``out_dtype``, tau [H, T] fp32; rows outside all sequences are left as
+    they were."""
+    qs = _rows("Q", Q, None, None)
+    T, H, D = Q.shape
+    ks = _rows("K", K, None, Q.device)
+    Hkv = K.shape[1]
+    vs = _rows("V", V, Hkv, Q.device)
+    if K.shape[0] != T or V.shape[0] != T:
+        raise ValueError("Q, K and V have %d, %d and %d tokens" % (T, K.shape[0], V.shape[0]))
+    n = cu.shape[0] - 1 if isinstance(cu, torch.Tensor) and cu.dim() == 1 else -1
+    _need("cu", cu, (n + 1,), torch.int32, Q.device)
+    code = _out_code(out_dtype)
+    with _on(Q.device):
+        if O is None:
+            O = torch.empty((T, H, D), dtype=out_dtype, device=Q.device)
+        else:
+            _need("O", O, (T, H, D), out_dtype, Q.device)
+        if tau is None:
+            tau = torch.empty((H, T), dtype=torch.float32, device=Q.device)
+        else:
+            _need("tau", tau, (H, T), torch.float32, Q.device)
+        _raise(lib.entmax_attn_prompt(Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, cu.data_ptr(), n, T,
+                                      int(max_len), float(D ** -0.5 if scale is None else scale), float(alpha), H,
+                                      Hkv, D, O.data_ptr(), code, tau.data_ptr(), _handle(stream, Q.device)),
+               "entmax_attn_prompt")
+    return O, tau

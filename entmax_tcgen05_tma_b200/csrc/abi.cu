@@ -197,6 +197,24 @@ cudaError_t make_tile_map(CUtensorMap* map, const void* base, int layout, int B,
     return r == CUDA_ERROR_INVALID_CONTEXT ? cudaErrorDeviceUninitialized : cudaErrorInvalidValue;
 }
 
+cudaError_t make_packed_map(CUtensorMap* map, const void* base, int heads, long long stride, int T, int box_rows) {
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        cudaError_t e = driver_fn(&g_encode, "cuTensorMapEncodeTiled", 12000);
+        if (e != cudaSuccess) return e;
+    }
+    // (d, head, token): boxes of one head by box_rows tokens
+    const cuuint64_t dims[3] = {(cuuint64_t)HEAD_DIM, (cuuint64_t)heads, (cuuint64_t)T};
+    const cuuint64_t strides[2] = {(cuuint64_t)HEAD_DIM * 2, (cuuint64_t)stride * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)HEAD_DIM, 1u, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r == CUDA_SUCCESS) return cudaSuccess;
+    return r == CUDA_ERROR_INVALID_CONTEXT ? cudaErrorDeviceUninitialized : cudaErrorInvalidValue;
+}
+
 }  // namespace entmax
 
 using namespace entmax;

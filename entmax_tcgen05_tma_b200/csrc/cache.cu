@@ -8,6 +8,7 @@
 #include <cuda_bf16.h>
 #include <mutex>
 #include "cache.cuh"
+#include "common.cuh"
 #include "internal.h"
 
 namespace entmax {
@@ -374,27 +375,8 @@ __global__ void __launch_bounds__(256) fork_kernel(const CacheArgs c, const int*
 }
 
 // ---------------------------------------------------------------------------------------- append
-// First page item of entry i: entry i touches at most (m + 126) / 64 pages for its m tokens, so items
-// (cu_i + 126 i) / 64 .. are its own (the differences of these are at least that).
-__device__ __forceinline__ long long item_base(int cu, int i) { return ((long long)cu + 126ll * i) / 64; }
-long long item_bound(int n, int T) { return ((long long)T + 126ll * n) / 64 + 1; }
-
-// The entry that item w belongs to: the last i in [0, n) with item_base(i) <= w, by a 33-ary search of the
-// warp (cu does not decrease).
-__device__ __forceinline__ int find_entry(const int* __restrict__ cu, int n, long long w) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = n;  // the answer lies in [lo, hi)
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 32) / 33;
-        const int i = lo + (lane + 1) * step;
-        const bool ok = i < hi && item_base(cu[i], i) <= w;
-        const int k = __popc(__ballot_sync(0xffffffffu, ok));  // probes that hold come first
-        const int next = min(hi, lo + (k + 1) * step);
-        lo += k * step;
-        hi = next;
-    }
-    return lo;
-}
+// Entry i touches at most (m + 126) / 64 pages for its m tokens.
+constexpr int PAGE_ADD = 2 * (PAGE - 1);
 
 // One warp per (page, K or V, head) block.  A new token's row of a head is 128 bytes in and 64 bytes out: 8
 // lanes read and write a row, 16 bytes and 8 bytes each, so a warp moves four rows per step and holds a
@@ -410,9 +392,9 @@ __global__ void __launch_bounds__(256) append_kernel(const CacheArgs c, int laye
     const long long item = w / per;
     if (item >= items) return;
     const int rest = (int)(w - item * per), is_v = rest >= c.Hkv, head = rest - (is_v ? c.Hkv : 0);
-    const int i = find_entry(cu, n, item);
+    const int i = find_packed(cu, n, item, PAGE, PAGE_ADD);
     const int c0 = cu[i], c1 = cu[i + 1], s = seqs[i];
-    const long long k = item - item_base(c0, i);
+    const long long k = item - unit_base(c0, i, PAGE, PAGE_ADD);
     if (c0 == c1 || k < 0) return;
     bool bad = c0 < 0 || c1 < c0 || c1 > T || s < 0 || s >= c.n_seqs;
     if (!bad) {
@@ -526,6 +508,8 @@ __global__ void __launch_bounds__(256) append_kernel(const CacheArgs c, int laye
 
 }  // namespace
 
+cudaError_t serving_status_ptr(int** out) { return cache_status_ptr(out); }
+
 int cache_args(const entmax_cache* c, CacheArgs* out) {
     if (!c) return ENTMAX_ERR_ARG;
     if (c->n_layers < 1 || c->n_pages < 1 || c->H_kv < 1 || c->n_seqs < 1 || c->max_pages < 1) return ENTMAX_ERR_ARG;
@@ -628,7 +612,7 @@ int entmax_cache_append(const entmax_cache* c, int layer, const void* K, long lo
     CacheArgs a;
     rc = cache_args(c, &a);
     if (rc || n == 0 || T == 0) return rc;
-    const long long items = item_bound(n, T), warps = items * 2 * c->H_kv;
+    const long long items = unit_base(T, n, PAGE, PAGE_ADD) + 1, warps = items * 2 * c->H_kv;
     if ((warps + 7) / 8 > 0x7fffffffll) return ENTMAX_ERR_UNSUPPORTED;
     append_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a, layer, static_cast<const uint16_t*>(K), k_stride,
                                                                   static_cast<const uint16_t*>(V), v_stride, seqs, cu,

@@ -38,6 +38,7 @@ constexpr uint16_t FULL_BLOCK = 0x8000u;  // block-list flag: every key allowed 
 // device status codes (mirror entmax_status in include/entmax_attn.h)
 constexpr int STATUS_OK = 0;
 constexpr int STATUS_TIMEOUT = -4;
+constexpr int STATUS_BAD_ARG = -1;
 
 struct WaitCfg {
     int* status;                   // device status word (global)
@@ -126,6 +127,23 @@ __device__ __forceinline__ uint32_t range_bits(int jc, int lo, int hi) {
     const int lb = max(a, 0), hb = min(b, 31);
     const uint32_t upper = hb == 31 ? 0xffffffffu : ((1u << (hb + 1)) - 1u);
     return upper & ~((1u << lb) - 1u);
+}
+
+// The packed sequence that unit w (of `unit` tokens, unit_base) belongs to: the last i in [0, n) with
+// unit_base(cu_i, i) <= w, by a 33-ary search of the warp (cu does not decrease).
+__device__ __forceinline__ int find_packed(const int* __restrict__ cu, int n, long long w, int unit, int add) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = n;  // the answer lies in [lo, hi)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 32) / 33;
+        const int i = lo + (lane + 1) * step;
+        const bool ok = i < hi && unit_base(cu[i], i, unit, add) <= w;
+        const int k = __popc(__ballot_sync(0xffffffffu, ok));  // probes that hold come first
+        const int next = min(hi, lo + (k + 1) * step);
+        lo += k * step;
+        hi = next;
+    }
+    return lo;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) {

@@ -358,8 +358,8 @@ __device__ __forceinline__ float block_max(float a, float* red) {
 template <bool GEN>
 __device__ __noinline__ void fallback_row(const __nv_bfloat16* __restrict__ Q, const __nv_bfloat16* __restrict__ K,
                                           const __nv_bfloat16* __restrict__ V, const uint32_t* bits, float* sbuf,
-                                          float* red, HeadRef hq, HeadRef hkv, int bh, int i, int L,
-                                          int causal, int window, float scale, float am1, int nallow, void* O,
+                                          float* red, HeadRef hq, HeadRef hk, HeadRef hvv, HeadRef ho, size_t tau0,
+                                          int bh, int i, int L, int causal, int window, float scale, float am1, int nallow, void* O,
                                           int out_f32, float* tau, float* otil, float* rsum) {
     const int tid = threadIdx.x;
     float* qf = red + 64;  // 64 floats (red[0..63] holds reduction partials)
@@ -374,7 +374,7 @@ __device__ __noinline__ void fallback_row(const __nv_bfloat16* __restrict__ Q, c
         const int j = lo + e;
         float s = -INFINITY;
         if ((bits[j >> 5] >> (j & 31)) & 1u) {
-            const uint4* kr = reinterpret_cast<const uint4*>(K + hkv.row(j) * HEAD_DIM);
+            const uint4* kr = reinterpret_cast<const uint4*>(K + hk.row(j) * HEAD_DIM);
             float acc = 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -522,7 +522,7 @@ __device__ __noinline__ void fallback_row(const __nv_bfloat16* __restrict__ Q, c
                 hv = 0.5f * (s - t);
                 p = hv * hv;
             }
-            const float v = __bfloat162float(V[hkv.row(lo + e) * HEAD_DIM + d]);
+            const float v = __bfloat162float(V[hvv.row(lo + e) * HEAD_DIM + d]);
             acc = fmaf(p, v, acc);
             acc2 = fmaf(hv, v, acc2);
             hsum += hv;
@@ -535,10 +535,10 @@ __device__ __noinline__ void fallback_row(const __nv_bfloat16* __restrict__ Q, c
         float o = 0.f;
 #pragma unroll
         for (int p = 0; p < PH; ++p) o += red[tid + p * HEAD_DIM];
-        const size_t oi = hq.row(i) * HEAD_DIM + tid;
+        const size_t oi = ho.row(i) * HEAD_DIM + tid;
         if (out_f32) reinterpret_cast<float*>(O)[oi] = o;
         else reinterpret_cast<__nv_bfloat16*>(O)[oi] = __float2bfloat16_rn(o);
-        if (tid == 0) tau[(size_t)bh * L + i] = GEN ? m + t * ex : t;
+        if (tid == 0) tau[tau0 + i] = GEN ? m + t * ex : t;
     }
     if (aux) {  // uniform across the CTA
         __syncthreads();
@@ -632,7 +632,10 @@ __device__ __noinline__ void mma_half(PipeCtl* ctl, const WaitCfg& wc, const uin
     ctl->nmma[p] = issued;  // drained at teardown if the CTA aborts (drain_half)
 }
 
-template <bool GEN, bool XT>
+// PK: packed sequences, causal (prompts).  CTA x takes a 128-row tile of some sequence, the last tiles of
+// the last sequences first (their rows have the most keys); rows, keys and lengths are then that
+// sequence's alone, and HeadRef's "batch 1 of length cu_i" places them among all tokens.
+template <bool GEN, bool XT, bool PK = false>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v, const AttnArgs args, const FwdOut out) {
@@ -655,17 +658,36 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
     PipeCtl* ctl = reinterpret_cast<PipeCtl*>(smem + OFF_CTL);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int L = args.L;
-    const int tile = blockIdx.x, bh = blockIdx.y;
-    const int b = bh / args.H;
+    int L = args.L, tile = blockIdx.x, first = 0;
+    const int bh = blockIdx.y;
+    const int b = PK ? 0 : bh / args.H;
+    if (PK) {
+        if (blockIdx.x == 0 && bh == 0)  // one CTA reports the sequences that are left out
+            for (int s = tid; s < args.n_seqs; s += NUM_THREADS) {
+                const int c0 = args.cu[s], c1 = args.cu[s + 1];
+                if (c0 < 0 || c1 < c0 || c1 > args.T || c1 - c0 > args.max_len) atomicExch(args.arg_status, STATUS_BAD_ARG);
+            }
+        const long long unit = (long long)gridDim.x - 1 - blockIdx.x;
+        const int s = find_packed(args.cu, args.n_seqs, unit, TILE, TILE - 1);
+        first = args.cu[s];
+        const int end = args.cu[s + 1];
+        tile = (int)(unit - unit_base(first, s, TILE, TILE - 1));
+        L = end - first;
+        if (first < 0 || L < 0 || end > args.T || L > args.max_len || tile < 0 || (long long)tile * TILE >= L) return;
+    }
     const int bhk = kv_head_of(bh, args.H, args.Hkv);  // K/V head (b * Hkv + index)
-    const HeadRef hq{args.layout, b, bh - b * args.H, args.H, L};          // rows of Q and O
-    const HeadRef hkv{args.layout, b, bhk - b * args.Hkv, args.Hkv, L};    // rows of K and V
+    // rows of Q, K, V and O
+    const HeadRef hq = PK ? HeadRef{1, 1, bh, args.q_step, first} : HeadRef{args.layout, b, bh - b * args.H, args.H, L};
+    const HeadRef hkv = PK ? HeadRef{1, 1, bhk, args.k_step, first}
+                           : HeadRef{args.layout, b, bhk - b * args.Hkv, args.Hkv, L};
+    const HeadRef hv = PK ? HeadRef{1, 1, bhk, args.v_step, first} : hkv;
+    const HeadRef ho = PK ? HeadRef{1, 1, bh, args.H, first} : hq;
+    const size_t tau0 = PK ? (size_t)bh * args.T + first : (size_t)bh * L;  // tau of row i at tau0 + i
     const int i0 = tile * TILE;
     const WaitCfg wc{args.status, args.timeout_ns};
     // V row j of this head at Vh + j * vstep
-    const __nv_bfloat16* Vh = reinterpret_cast<const __nv_bfloat16*>(args.V) + hkv.row(0) * HEAD_DIM;
-    const size_t vstep = hkv.step() * HEAD_DIM;
+    const __nv_bfloat16* Vh = reinterpret_cast<const __nv_bfloat16*>(args.V) + hv.row(0) * HEAD_DIM;
+    const size_t vstep = hv.step() * HEAD_DIM;
 
     if (tid == 0) {
         mbar_init(smem_u32(vbar), 1);
@@ -806,11 +828,11 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         // no allowed key) cuts everything.
         float t;
         if (XT) {
-            t = i < L ? out.tau[(size_t)bh * L + i] / scale : INFINITY;
+            t = i < L ? out.tau[tau0 + i] / scale : INFINITY;
             if (isfinite(t)) t -= fabsf(t) * 0x1p-20f;
         } else {
             t = GEN ? gen_bound(a0, a1, a2, a3, wk, am1, ex, scale)
-                    : fmaxf(a0 - two_over_scale, top4_bound(a0, a1, a2, a3, c4));
+                    : fmaxf(a0 - two_over_scale, top4_bound<PK>(a0, a1, a2, a3, c4));
         }
 
         // ---------------- pass B: candidates s > m - 2 (scaled) into this warpgroup's partition
@@ -904,7 +926,7 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         const int nh = mode == 0 ? (h == 0 ? s0.n : s1.n) : 0;
         float* pcv = cv + h * CAPW * TILE;
         uint16_t* pcj = cj + h * CAPW * TILE;
-        const float tau_i = nh > 0 ? out.tau[(size_t)bh * L + i] : 0.f;
+        const float tau_i = nh > 0 ? out.tau[tau0 + i] : 0.f;
         int sn = 0;
         for (int k = 0; k < nh; ++k) {
             const float d = fmaf(scale, pcv[k * TILE + r], -tau_i);  // S_ij - tau_i (scaled)
@@ -954,7 +976,7 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         top4_insert(s1.a2, b0, b1, b2, b3);
         top4_insert(s1.a3, b0, b1, b2, b3);
         const float t_cut = GEN ? gen_bound(b0, b1, b2, b3, wk, am1, ex, scale)
-                                : fmaxf(b0 - two_over_scale, top4_bound(b0, b1, b2, b3, c4));
+                                : fmaxf(b0 - two_over_scale, top4_bound<PK>(b0, b1, b2, b3, c4));
         // general alpha, in y units: g(-1) >= 1 from the max alone, g(-k^(-am1)) <= 1 over k candidates
         const float hi = GEN ? -pow_pos((float)max(s0.n + s1.n, 1), -am1) : -2.f / sqrtf((float)max(s0.n + s1.n, 1));
         const float lo = GEN ? fminf(fmaxf(-1.f, am1 * fmaf(scale, t_cut, -ms)), hi)
@@ -1019,13 +1041,13 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
                 keep(c1, j1);
             }
             supp_cnt[h * TILE + r] = sn;
-            if (h == 0) out.tau[(size_t)bh * L + i] = GEN ? ms + tau_x * ex : ms + tau_x;
+            if (h == 0) out.tau[tau0 + i] = GEN ? ms + tau_x * ex : ms + tau_x;
         } else if (mode == 2) {
             if (h == 0) atomicOr(&redo[r >> 5], 1u << (r & 31));
             supp_cnt[h * TILE + r] = 0;
         } else {
             supp_cnt[h * TILE + r] = 0;
-            if (h == 0 && i < L) out.tau[(size_t)bh * L + i] = INFINITY;  // no allowed key: O_i = 0
+            if (h == 0 && i < L) out.tau[tau0 + i] = INFINITY;  // no allowed key: O_i = 0
         }
         __syncwarp();
         if (out.save.row_cnt)
@@ -1090,7 +1112,7 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
                         for (int c = 0; c < 4; ++c) fma_bf16x8(acc[c], pw[u], x[u][c]);
                 }
             }
-            const size_t oi = hq.row(i) * HEAD_DIM + 32 * h;
+            const size_t oi = ho.row(i) * HEAD_DIM + 32 * h;
             if (out.out_f32) {
                 float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(out.O) + oi);
 #pragma unroll
@@ -1160,7 +1182,8 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
                 mask &= mask - 1;
                 fallback_row<GEN>(reinterpret_cast<const __nv_bfloat16*>(args.Q),
                                   reinterpret_cast<const __nv_bfloat16*>(args.K),
-                                  reinterpret_cast<const __nv_bfloat16*>(args.V), bits, scratch, red, hq, hkv, bh,
+                                  reinterpret_cast<const __nv_bfloat16*>(args.V), bits, scratch, red, hq, hkv, hv, ho,
+                                  tau0, bh,
                                   i0 + rr, L, args.causal, args.window, scale, am1,
                                   rows[rr].nallow + rows[TILE + rr].nallow, out.O, out.out_f32, out.tau,
                                   out.otil, out.rsum);
@@ -1193,6 +1216,21 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
 }
 
 }  // namespace
+
+cudaError_t launch_fwd_packed(const AttnArgs& a, const FwdOut& o, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = make_packed_map(&mq, a.Q, a.H, 64ll * a.q_step, a.T, TILE);
+    if (e == cudaSuccess) e = make_packed_map(&mk, a.K, a.Hkv, 64ll * a.k_step, a.T, BLK);
+    if (e == cudaSuccess) e = make_packed_map(&mv, a.V, a.Hkv, 64ll * a.v_step, a.T, BLK);
+    if (e != cudaSuccess) return e;
+    const bool gen = generic_alpha(a);
+    const auto f = gen ? entmax_fwd_kernel<true, false, true> : entmax_fwd_kernel<false, false, true>;
+    e = ensure_smem_attr(reinterpret_cast<const void*>(f), SMEM_BYTES, gen ? 20 : 19);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(unit_base(a.T, a.n_seqs, TILE, TILE - 1) + 1), a.H);
+    f<<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(mq, mk, mv, a, o);
+    return cudaGetLastError();
+}
 
 size_t fwd_smem_bytes() { return SMEM_BYTES; }
 

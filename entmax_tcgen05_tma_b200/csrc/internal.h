@@ -23,7 +23,17 @@ struct AttnArgs {
     float am1;               // alpha - 1 in (0, 1]: p = max(0, am1 (S - tau))^(1 / am1); 0.5 is 1.5-entmax.
                              // 0: softmax, p = exp(S - tau) with tau = log sum_j exp(S_ij)
     int layout;              // 0: Q, K, V, O, dO, dQ, dK, dV are [B, heads, L, 64]; 1: [B, L, heads, 64]
+    // Packed sequences (prompts; the forward's PK instantiations and prompt.cu alone): token t's head h of
+    // a tensor lies at 64 (t step + h); sequence i has the tokens cu[i] .. cu[i + 1] - 1; tau is [H][T].
+    const int* cu;
+    int n_seqs, T, max_len;
+    int q_step, k_step, v_step;  // token strides in units of 64 elements
+    int* arg_status;             // word that records sequences out of range
 };
+
+// Packed sequences in units of `unit` tokens: where sequence i touches at most (len_i + add) / unit units, the
+// numbers unit_base(cu_i, i) .. unit_base(cu_i+1, i + 1) - 1 are its own (there are at least that many).
+__host__ __device__ __forceinline__ long long unit_base(int cu, long long i, int unit, int add) { return (cu + add * i) / unit; }
 
 // One head of a [B, nh, L, 64] (layout 0) or [B, L, nh, 64] (layout 1) tensor: its memory rows
 // (units of 64 elements) and the TMA coordinates of a box of its rows.  Layout 0 maps are
@@ -107,6 +117,13 @@ cudaError_t launch_bwd_saved(const AttnArgs& a, const BwdIO& io, const SavedSupp
 // Tensor map over a [B*H, L, 64] bf16 tensor, boxes of box_rows rows, 128-byte swizzle.
 cudaError_t make_tile_map(CUtensorMap* map, const void* base, int layout, int B, int nh, int L, int box_rows);
 
+// The same over packed tokens: [T][heads][64] bf16 with a token stride (in elements, a multiple of 8).
+cudaError_t make_packed_map(CUtensorMap* map, const void* base, int heads, long long stride, int T, int box_rows);
+
+// Prompts (a.cu set): alpha != 1 through the gather forward, softmax through prompt.cu.
+cudaError_t launch_fwd_packed(const AttnArgs& a, const FwdOut& o, cudaStream_t stream);
+cudaError_t launch_prompt_softmax(const AttnArgs& a, const FwdOut& o, cudaStream_t stream);
+
 // Gather forward (fwd.cu).  extract: support extraction for a backward given tau alone -- o.tau is
 // read (the caller's tau), o.save receives the support lists, o.O, o.otil and o.rsum are unused.
 cudaError_t launch_fwd(const AttnArgs& a, const FwdOut& o, cudaStream_t stream, bool extract = false);
@@ -137,6 +154,8 @@ cudaError_t abi_current_device(int* dev);
 int abi_record(cudaError_t e);
 cudaError_t abi_status_ptr(int** out);
 unsigned long long abi_timeout_ns();
+// cache.cu: the word that records entries that the serving path left out.
+cudaError_t serving_status_ptr(int** out);
 
 // Raises a kernel's dynamic shared-memory limit once per (kernel slot, device).
 cudaError_t ensure_smem_attr(const void* func, int bytes, int slot);

@@ -1,6 +1,6 @@
 /*
- * entmax_cache.h -- C ABI of the serving path: a paged key/value cache held in 8 bits, and the
- * attention of single tokens over it.  (Prompts: entmax_attn_prompt in entmax_attn.h.)
+ * entmax_cache.h -- C ABI of the serving path: attention over packed prompts, a paged key/value
+ * cache held in 8 bits, and the attention of single tokens over it.
  *
  * The AdaSplash pages describe encoders and a causal decoder layer that recompute every key and
  * value; they print no cache.  The weights are those of the other entry points: for query head h of
@@ -126,6 +126,26 @@ ENTMAX_API int entmax_cache_attn(const entmax_cache* c, int layer, const void* Q
                                  const int32_t* seqs, int n, int max_len, float scale, float alpha, int H, void* O,
                                  int out_dtype, float* tau, void* workspace, size_t ws_bytes, cudaStream_t stream);
 ENTMAX_API size_t entmax_cache_attn_workspace_size(int n, int H, int H_kv, float alpha);
+
+/*
+ * Attention over whole prompts: packed sequences of different lengths, causal, grouped heads.  For row i of
+ * a sequence and the keys j <= i of the same sequence, the weights and outputs of entmax_attn_fwd_ex.
+ *   Q            bf16, token t's head h at [t * q_stride + 64 h]; K, V the same with H_kv heads.  Strides in
+ *                elements, multiples of 64, at least 64 times the heads (a slice of a fused projection has
+ *                them); 16-byte aligned.
+ *   cu           device int32 [n + 1], not decreasing, cu[n] <= T: sequence i has the tokens cu[i] .. cu[i+1] - 1.
+ *                Tokens outside all sequences are neither read as keys nor written.
+ *   max_len      no sequence is longer; at most 16384, for softmax 1048576 (else ENTMAX_ERR_UNSUPPORTED).
+ *                A sequence that is longer, or lies outside [0, T], is left out.
+ *   alpha        in [1, 2] as in entmax_attn_fwd_ex (within 1e-4 of 1: softmax).
+ *   O            [T][H][64] bf16 or fp32, 16-byte aligned; tau [H][T] fp32.
+ * Softmax weights multiply the values as one bf16 number for a bf16 output and as three (24 bits) for
+ * an fp32 output.  n <= 4096.  Results are the same bit for bit from run to run.
+ */
+ENTMAX_API int entmax_attn_prompt(const void* Q, long long q_stride, const void* K, long long k_stride, const void* V,
+                                  long long v_stride, const int32_t* cu, int n, int T, int max_len, float scale,
+                                  float alpha, int H, int H_kv, int D, void* O, int out_dtype, float* tau,
+                                  cudaStream_t stream);
 
 /* Synchronises `stream`, then returns and clears the cache status word of the current device: ENTMAX_OK,
  * or ENTMAX_ERR_ARG if a kernel left an entry out since the last read. */

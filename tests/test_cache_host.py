@@ -95,6 +95,26 @@ def test_attn_workspace_size():
     assert 0 < size(1, 4, 4, 1.0) <= size(4096, 4, 4, 1.0) and size(1, 4, 4, 1.5) < size(64, 4, 4, 1.5) < size(64, 8, 4, 1.5)
 
 
+def prompt(**kw):
+    a = dict(Q=P, qs=256, K=P, ks=128, V=P, vs=128, cu=P, n=2, T=10, max_len=8, scale=0.125, alpha=1.5, H=4, Hkv=2, D=64, O=P, out=0, tau=P)
+    a.update(kw)
+    return E.lib.entmax_attn_prompt(*a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(n=-1), E.ENTMAX_ERR_ARG), (dict(T=-1), E.ENTMAX_ERR_ARG), (dict(max_len=-1), E.ENTMAX_ERR_ARG),
+    (dict(n=4097), E.ENTMAX_ERR_UNSUPPORTED), (dict(max_len=16385), E.ENTMAX_ERR_UNSUPPORTED), (dict(D=128), E.ENTMAX_ERR_UNSUPPORTED),
+    (dict(max_len=(1 << 20) + 1, alpha=1.0), E.ENTMAX_ERR_UNSUPPORTED), (dict(H=3), E.ENTMAX_ERR_ARG), (dict(H=0), E.ENTMAX_ERR_ARG),
+    (dict(H=0, Hkv=0), E.ENTMAX_OK), (dict(n=0), E.ENTMAX_OK), (dict(T=0), E.ENTMAX_OK), (dict(alpha=2.01), E.ENTMAX_ERR_ARG),
+    (dict(alpha=float("nan")), E.ENTMAX_ERR_ARG), (dict(scale=float("inf")), E.ENTMAX_ERR_ARG), (dict(out=5), E.ENTMAX_ERR_ARG),
+    (dict(Q=None), E.ENTMAX_ERR_ARG), (dict(K=P + 8), E.ENTMAX_ERR_ARG), (dict(V=None), E.ENTMAX_ERR_ARG), (dict(cu=None), E.ENTMAX_ERR_ARG),
+    (dict(O=P + 8), E.ENTMAX_ERR_ARG), (dict(tau=P + 2), E.ENTMAX_ERR_ARG), (dict(qs=192), E.ENTMAX_ERR_ARG), (dict(ks=136), E.ENTMAX_ERR_ARG),
+    (dict(vs=64), E.ENTMAX_ERR_ARG),
+])
+def test_bad_prompt_arguments(kw, code):
+    assert prompt(**kw) == code
+
+
 def test_workspace_size_grows_with_the_pool():
     small, large = cache(n_pages=8), cache(n_pages=100000)
     a, b = (E.lib.entmax_cache_workspace_size(ctypes.addressof(x)) for x in (small, large))

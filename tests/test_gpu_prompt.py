@@ -1,0 +1,271 @@
+"""Attention over packed prompts against fp64.
+
+Tolerances.  Scores are sums of 64 exact products in fp32, scaled once: |dS| <= delta = 2^-18 (1 + max|S|).
+  softmax, fp32 output:  a weight has the relative error 2 delta + 2^-20 (exp2, sums; three bf16 parts: 2^-24), so
+               |dO| <= (2 delta + 2^-20) sum p |V|.
+  softmax, bf16 output:  2 delta + 2^-8 (one bf16 part, half a step) + 2^-18 (exponentials from a polynomial: 2.8e-6),
+               then the output's own rounding, 2^-8 |O|.   |dtau| <= delta + 2^-18 (1 + |tau|) for both.
+  1.5-entmax and other alpha: the suite's flat bounds (gpu_helpers): 1e-2 on the fp32 output, 1e-3 on tau; the bf16
+               output is the fp32 output rounded.
+"""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import O_TOL, TAU_TOL, assert_bf16_is_rounded
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def inputs(T, H, H_kv, seed=0, fused=False):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn((T, H + 2 * H_kv, 64), generator=g, device="cuda").to(torch.bfloat16)
+    Q, K, V = x[:, :H], x[:, H:H + H_kv], x[:, H + H_kv:]
+    return (Q, K, V) if fused else (Q.contiguous(), K.contiguous(), V.contiguous())
+
+
+def starts(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def reference(Q, K, V, lens, scale, alpha, first=0):
+    """fp64 O [T, H, 64], tau [H, T], sum p |V| and max |S| by row (numpy), for the rows of the sequences."""
+    from oracle import oracle as orc
+    q, k, v = (t.double().cpu().numpy() for t in (Q, K, V))
+    T, H = q.shape[:2]
+    G = H // k.shape[1]
+    O, tau = np.zeros((T, H, 64)), np.full((H, T), np.inf)
+    A, M = np.zeros((T, H, 64)), np.zeros((H, T))
+    at = first
+    for n in lens:
+        for h in range(H):
+            S = scale * (q[at:at + n, h] @ k[at:at + n, h // G].T)
+            S[np.triu_indices(n, 1)] = -np.inf
+            V_ = v[at:at + n, h // G]
+            if alpha == 1.0 and n:
+                m = S.max(1, keepdims=True)
+                t = m + np.log(np.exp(S - m).sum(1, keepdims=True))
+                P = np.exp(S - t)
+                tau[h, at:at + n] = t[:, 0]
+                O[at:at + n, h] = P @ V_
+                A[at:at + n, h] = P @ np.abs(V_)
+                M[h, at:at + n] = np.abs(np.where(np.isinf(S), 0, S)).max(1)
+        at += n
+    if alpha != 1.0:
+        at = first
+        rep = lambda x: np.repeat(x, G, axis=1)  # noqa: E731
+        for n in lens:
+            if n:
+                one = lambda x: np.ascontiguousarray(x[at:at + n].transpose(1, 0, 2)[None])  # noqa: E731, B023
+                o, t = orc.attn_fwd(one(q), one(rep(k)), one(rep(v)), None, True, 0, scale, alpha=alpha)
+                O[at:at + n] = o[0].transpose(1, 0, 2)
+                tau[:, at:at + n] = t[0]
+            at += n
+    return O, tau, A, M
+
+
+def check(Q, K, V, lens, out, scale, alpha, first=0):
+    (O32, tau32), (O16, tau16) = out
+    O, tau, A, M = reference(Q, K, V, lens, scale, alpha, first)
+    rows = slice(first, first + sum(lens))
+    o32, o16, t32, t16 = (x.double().cpu().numpy() for x in (O32, O16, tau32, tau16))
+    if alpha == 1.0:
+        delta = 2.0 ** -18 * (1 + M.T[rows, :, None])
+        assert (np.abs(o32 - O)[rows] <= (2 * delta + 2.0 ** -20) * A[rows]).all(), np.abs(o32 - O)[rows].max()
+        assert (np.abs(o16 - O)[rows] <= (2 * delta + 2.0 ** -8 + 2.0 ** -18) * A[rows] * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(O[rows])).all()
+        for t in (t32, t16):
+            assert (np.abs(t - tau)[:, rows] <= delta[:, :, 0].T + 2.0 ** -18 * (1 + np.abs(tau[:, rows]))).all()
+    else:
+        assert np.abs(o32 - O)[rows].max() <= O_TOL and np.abs(t32 - tau)[:, rows].max() <= TAU_TOL
+        assert_bf16_is_rounded(O16[rows], O32[rows])
+        assert torch.equal(tau32[:, rows], tau16[:, rows])
+
+
+def both(Q, K, V, cu, max_len, **kw):
+    import entmax_tcgen05_tma_b200 as E
+    T, H = Q.shape[:2]
+    out = []
+    for dt in (torch.float32, torch.bfloat16):
+        O = torch.full((T, H, 64), 7.0, dtype=dt, device="cuda")  # rows outside all sequences stay
+        tau = torch.full((H, T), 7.0, device="cuda")
+        out.append(E.entmax_attn_prompt(Q, K, V, ints(cu), max_len, out_dtype=dt, O=O, tau=tau, **kw))
+    return out
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5, 1.25, 2.0])
+@pytest.mark.parametrize("lens,H,H_kv,fused", [
+    ([1], 1, 1, False), ([128], 2, 1, True), ([129], 3, 3, True), ([256, 1, 257], 4, 2, False), ([127, 128, 0, 0, 129, 64], 2, 2, True),
+    ([700, 3, 40, 511, 513], 6, 2, True), ([1, 1, 1, 1, 1, 1], 5, 1, False), ([0, 300, 0], 8, 1, True),
+])
+def test_lengths_and_heads(alpha, lens, H, H_kv, fused):
+    import entmax_tcgen05_tma_b200 as E
+    cu = starts(lens)
+    Q, K, V = inputs(cu[-1], H, H_kv, len(lens), fused)
+    out = both(Q, K, V, cu, max(lens), scale=0.125, alpha=alpha)
+    check(Q, K, V, lens, out, 0.125, alpha)
+    assert E.entmax_attn_device_status() == 0 and E.entmax_cache_status() == 0
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_many_short_sequences(alpha):
+    rng = random.Random(4)
+    lens = [rng.randint(0, 90) for _ in range(400)]
+    cu = starts(lens)
+    Q, K, V = inputs(cu[-1], 2, 1, 5, True)
+    check(Q, K, V, lens, both(Q, K, V, cu, 2000, scale=0.25, alpha=alpha), 0.25, alpha)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_long_sequence(alpha):
+    lens = [2900, 2048]
+    cu = starts(lens)
+    Q, K, V = inputs(cu[-1], 4, 2, 6, True)
+    check(Q, K, V, lens, both(Q, K, V, cu, 2900, scale=0.125, alpha=alpha), 0.125, alpha)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 4.0])
+def test_flat_and_peaked_rows_and_rising_maxima(alpha, scale):
+    """Scores that grow along the keys: the running reference moves in many blocks."""
+    lens = [600, 333]
+    Q, K, V = inputs(933, 2, 2, 7)
+    K = (K.float() * torch.linspace(0.1, 4, 933, device="cuda")[:, None, None]).to(torch.bfloat16)
+    Q[5] = 0
+    check(Q, K, V, lens, both(Q, K, V, starts(lens), 600, scale=scale, alpha=alpha), scale, alpha)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_tokens_of_others_do_not_matter(alpha):
+    """NaN and infinities in every token outside the sequences, and in the next sequence."""
+    import entmax_tcgen05_tma_b200 as E
+    lens = [100, 129, 300]
+    cu = [70, 170, 299, 599]
+    Q, K, V = inputs(900, 4, 2, 8, True)
+    clean = both(Q, K, V, cu, 300, scale=0.125, alpha=alpha)
+    check(Q, K, V, lens, clean, 0.125, alpha, first=70)
+    for O, tau in clean:  # tokens outside are left as they were
+        assert (O[:70] == 7).all() and (O[599:] == 7).all() and (tau[:, :70] == 7).all() and (tau[:, 599:] == 7).all()
+    for x in (Q, K, V):
+        x[:70] = float("nan")
+        x[599:] = float("inf")
+        x[170:299] = float("nan")
+    spoiled = both(Q, K, V, cu, 300, scale=0.125, alpha=alpha)
+    for (a, t), (b, u) in zip(clean, spoiled):
+        for rows in (slice(70, 170), slice(299, 599)):
+            assert torch.equal(a[rows], b[rows]) and torch.equal(t[:, rows], u[:, rows])
+    assert E.entmax_attn_device_status() == 0
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_later_tokens_do_not_matter(alpha):
+    """A huge finite later token leaves the rows before it as they were, bit for bit."""
+    Q, K, V = inputs(400, 2, 1, 9)
+    a = both(Q, K, V, [0, 400], 400, scale=0.125, alpha=alpha)
+    K[333] = 100
+    V[333] = 3e38
+    b = both(Q, K, V, [0, 400], 400, scale=0.125, alpha=alpha)
+    for (x, t), (y, u) in zip(a, b):
+        assert torch.equal(x[:333], y[:333]) and torch.equal(t[:, :333], u[:, :333])
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_sequences_out_of_range_are_left_out(alpha):
+    import entmax_tcgen05_tma_b200 as E
+    Q, K, V = inputs(500, 2, 2, 10)
+    for cu, good in (([0, 100, 501], [0]), ([0, 100, 400], [0]), ([-5, 100, 300], [1]), ([0, 200, 100, 250], [0, 2])):
+        out = both(Q, K, V, cu, 200, scale=0.125, alpha=alpha)
+        assert E.entmax_cache_status() == E.ENTMAX_ERR_ARG and E.entmax_cache_status() == 0
+        if cu[-1] == 250:
+            continue  # decreasing starts overlap: nothing is promised but that memory stays whole
+        touched = torch.zeros(500, dtype=torch.bool)
+        for i in good:
+            lens = [cu[i + 1] - cu[i]]
+            check(Q, K, V, lens, out, 0.125, alpha, first=cu[i])
+            touched[cu[i]:cu[i + 1]] = True
+        for O, tau in out:
+            assert (O[~touched.cuda()] == 7).all() and (tau[:, ~touched.cuda()] == 7).all()
+    assert E.entmax_attn_device_status() == 0
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_same_bits_streams_and_graphs(alpha):
+    import entmax_tcgen05_tma_b200 as E
+    lens = [300, 17, 800]
+    cu = ints(starts(lens))
+    Q, K, V = inputs(1117, 6, 3, 11, True)
+    O, tau = E.entmax_attn_prompt(Q, K, V, cu, 800, alpha=alpha)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        O2, tau2 = E.entmax_attn_prompt(Q, K, V, cu, 16384, alpha=alpha)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        O3, tau3 = E.entmax_attn_prompt(Q, K, V, cu, 900, alpha=alpha)
+    g.replay()
+    torch.cuda.synchronize()
+    for x, t in ((O2, tau2), (O3, tau3)):
+        assert torch.equal(O, x) and torch.equal(tau, t)
+    cu.copy_(ints([0, 900, 900, 1000]))  # a replay takes the starts that it finds
+    g.replay()
+    O4, tau4 = E.entmax_attn_prompt(Q, K, V, cu, 900, alpha=alpha)
+    assert torch.equal(O3[:1000], O4[:1000]) and torch.equal(tau3[:, :1000], tau4[:, :1000])
+
+
+def test_wait_bound(alpha=1.0):
+    """A 1 ns bound makes the softmax kernel's waits give up: reported, and the next call is right."""
+    import entmax_tcgen05_tma_b200 as E
+    Q, K, V = inputs(3000, 8, 2, 12)
+    cu = [0, 1000, 3000]
+    E.entmax_attn_set_wait_timeout_ns(1)
+    try:
+        both(Q, K, V, cu, 2000, scale=0.125, alpha=1.0)
+        assert E.entmax_attn_device_status() == E.ENTMAX_ERR_TIMEOUT
+    finally:
+        E.entmax_attn_set_wait_timeout_ns(0)
+    check(Q[:, :2], K[:, :1], V[:, :1], [1000, 2000],
+          [(O[:, :2], t[:2]) for O, t in both(Q, K, V, cu, 2000, scale=0.125, alpha=1.0)], 0.125, 1.0)
+    assert E.entmax_attn_device_status() == 0
+
+
+def test_equals_the_dense_forward():
+    """One sequence, plain heads: the same weighting as entmax_attn_fwd_ex on the same causal problem."""
+    import entmax_tcgen05_tma_b200 as E
+    Q, K, V = inputs(1000, 4, 2, 13)
+    view = lambda x: x.transpose(0, 1)[None].contiguous()  # noqa: E731
+    for alpha in (1.0, 1.5):
+        O, tau = E.entmax_attn_prompt(Q, K, V, ints([0, 1000]), 1000, alpha=alpha, out_dtype=torch.float32)
+        D, u = E.entmax_attn_fwd_ex(view(Q), view(K), view(V), None, True, 0, None, alpha, out_dtype=torch.float32)
+        torch.testing.assert_close(O.transpose(0, 1)[None], D, rtol=1e-4, atol=1e-4)
+        torch.testing.assert_close(tau[None], u, rtol=1e-5, atol=1e-5)
+
+
+def test_refusals():
+    import entmax_tcgen05_tma_b200 as E
+    Q, K, V = inputs(100, 4, 2, 14)
+    cu = ints([0, 100])
+    for kw, code in ((dict(alpha=2.5), E.ENTMAX_ERR_ARG), (dict(alpha=0.5), E.ENTMAX_ERR_ARG), (dict(scale=0.0), E.ENTMAX_ERR_ARG),
+                     (dict(max_len=-1), E.ENTMAX_ERR_ARG), (dict(max_len=16385), E.ENTMAX_ERR_UNSUPPORTED),
+                     (dict(max_len=(1 << 20) + 1, alpha=1.0), E.ENTMAX_ERR_UNSUPPORTED)):
+        a = dict(max_len=100)
+        a.update(kw)
+        with pytest.raises(E.EntmaxError) as e:
+            E.entmax_attn_prompt(Q, K, V, cu, a.pop("max_len"), **a)
+        assert e.value.status == code
+    with pytest.raises(E.EntmaxError):  # 4 query heads on 3 key/value heads
+        E.entmax_attn_prompt(Q, inputs(100, 1, 3, 1)[1], inputs(100, 1, 3, 1)[1], cu, 100)
+    for bad in ((Q.float(), K, V), (Q, K[:50], V), (Q, K, V.transpose(0, 1)), (Q[..., :32], K, V), (Q, K[:, :, :32], V)):
+        with pytest.raises((TypeError, ValueError)):
+            E.entmax_attn_prompt(*bad, cu, 100)
+    with pytest.raises(TypeError):
+        E.entmax_attn_prompt(Q, K, V, cu.long(), 100)
+    O, tau = E.entmax_attn_prompt(Q[:0], K[:0], V[:0], ints([0]), 0)
+    assert O.shape == (0, 4, 64) and tau.shape == (4, 0)
