@@ -832,7 +832,7 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
             if (isfinite(t)) t -= fabsf(t) * 0x1p-20f;
         } else {
             t = GEN ? gen_bound(a0, a1, a2, a3, wk, am1, ex, scale)
-                    : fmaxf(a0 - two_over_scale, top4_bound<PK>(a0, a1, a2, a3, c4));
+                    : fmaxf(a0 - two_over_scale, top4_bound(a0, a1, a2, a3, c4));
         }
 
         // ---------------- pass B: candidates s > m - 2 (scaled) into this warpgroup's partition
@@ -976,7 +976,7 @@ entmax_fwd_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_consta
         top4_insert(s1.a2, b0, b1, b2, b3);
         top4_insert(s1.a3, b0, b1, b2, b3);
         const float t_cut = GEN ? gen_bound(b0, b1, b2, b3, wk, am1, ex, scale)
-                                : fmaxf(b0 - two_over_scale, top4_bound<PK>(b0, b1, b2, b3, c4));
+                                : fmaxf(b0 - two_over_scale, top4_bound(b0, b1, b2, b3, c4));
         // general alpha, in y units: g(-1) >= 1 from the max alone, g(-k^(-am1)) <= 1 over k candidates
         const float hi = GEN ? -pow_pos((float)max(s0.n + s1.n, 1), -am1) : -2.f / sqrtf((float)max(s0.n + s1.n, 1));
         const float lo = GEN ? fminf(fmaxf(-1.f, am1 * fmaf(scale, t_cut, -ms)), hi)
@@ -1223,9 +1223,8 @@ cudaError_t launch_fwd_packed(const AttnArgs& a, const FwdOut& o, cudaStream_t s
     if (e == cudaSuccess) e = make_packed_map(&mk, a.K, a.Hkv, 64ll * a.k_step, a.T, BLK);
     if (e == cudaSuccess) e = make_packed_map(&mv, a.V, a.Hkv, 64ll * a.v_step, a.T, BLK);
     if (e != cudaSuccess) return e;
-    const bool gen = generic_alpha(a);
-    const auto f = gen ? entmax_fwd_kernel<true, false, true> : entmax_fwd_kernel<false, false, true>;
-    e = ensure_smem_attr(reinterpret_cast<const void*>(f), SMEM_BYTES, gen ? 20 : 19);
+    const auto f = entmax_fwd_kernel<true, false, true>;  // 1.5-entmax and softmax: prompt.cu
+    e = ensure_smem_attr(reinterpret_cast<const void*>(f), SMEM_BYTES, 19);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(unit_base(a.T, a.n_seqs, TILE, TILE - 1) + 1), a.H);
     f<<<grid, NUM_THREADS, SMEM_BYTES, stream>>>(mq, mk, mv, a, o);

@@ -120,9 +120,9 @@ cudaError_t make_tile_map(CUtensorMap* map, const void* base, int layout, int B,
 // The same over packed tokens: [T][heads][64] bf16 with a token stride (in elements, a multiple of 8).
 cudaError_t make_packed_map(CUtensorMap* map, const void* base, int heads, long long stride, int T, int box_rows);
 
-// Prompts (a.cu set): alpha != 1 through the gather forward, softmax through prompt.cu.
+// Prompts (a.cu set): softmax and 1.5-entmax (prompt.cu), other alpha through the gather forward (fwd.cu).
 cudaError_t launch_fwd_packed(const AttnArgs& a, const FwdOut& o, cudaStream_t stream);
-cudaError_t launch_prompt_softmax(const AttnArgs& a, const FwdOut& o, cudaStream_t stream);
+cudaError_t launch_prompt(const AttnArgs& a, const FwdOut& o, cudaStream_t stream);
 
 // Gather forward (fwd.cu).  extract: support extraction for a backward given tau alone -- o.tau is
 // read (the caller's tau), o.save receives the support lists, o.O, o.otil and o.rsum are unused.

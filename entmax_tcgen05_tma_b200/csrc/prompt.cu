@@ -24,6 +24,7 @@
 #include <math.h>
 #include "../../include/entmax_cache.h"
 #include "common.cuh"
+#include "tau15.cuh"
 #include "internal.h"
 
 namespace entmax {
@@ -54,11 +55,15 @@ constexpr int O_CTL = O_LIST + LIST * (int)sizeof(Item);
 struct Ctl {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[NS], v_full[NS], kv_empty[NS];
-    uint64_t s_full[2], p_ready[2], o_full[2], o_empty[2];
+    uint64_t s_full[2];            // S of tile w is in TMEM
+    uint64_t s_done[2];            // its warps have read it and, in a last pass, stored P
+    uint64_t o_full[2], o_empty[2];
+    uint64_t voted[NS];            // the eight warps' votes on whether another pass of sums is needed
+    uint8_t vote[NS][8];
     uint32_t tmem_base;
     int abort_flag;
     int items;
-    int n_q, n_kv;                 // loads issued, for the drain after an abort
+    int n_q, n_k[NS], n_v[NS];     // loads issued
     uint32_t last_bar, last_par;   // the MMA thread's last commit
 };
 constexpr int PROMPT_SMEM = O_CTL + (int)sizeof(Ctl) + 1024;
@@ -100,6 +105,26 @@ __device__ __forceinline__ uint64_t f2exp2_poly(uint64_t x) {
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Maximum of a 32-value chunk that keeps a NaN (max32 does not).
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max32_nan(const float (&v)[32]) {
+    float m[11];
+#pragma unroll
+    for (int k = 0; k < 10; ++k) m[k] = max3_nan(v[3 * k], v[3 * k + 1], v[3 * k + 2]);
+    m[10] = max3_nan(v[30], v[31], v[31]);
+    const float a = max3_nan(m[0], m[1], m[2]), b = max3_nan(m[3], m[4], m[5]), c = max3_nan(m[6], m[7], m[8]);
+    return max3_nan(max3_nan(a, b, c), m[9], m[10]);
+}
+// 1 for x > 0, else 0.
+__device__ __forceinline__ float above0(float x) {
+    float r;
+    asm("set.gt.f32.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -208,10 +233,48 @@ __device__ __forceinline__ void make_list(const AttnArgs& a, long long first_ite
     if (tid == 0) ctl->items = n;
 }
 
-template <bool kF32>
+// The threshold iteration of 1.5-entmax for one row: the root t of g(t) = sum max(0, S - t)^2 = 4, from sums
+// over the scores above the present t.
+//   Newton's step is a lower bound of the root from either side (g is convex and decreasing); its error is of
+//   second order, (e / d)^2 / 2 for an error e before and a mean depth d = s2 / s1 of the support.
+//   The root of sum_{S > t} (S - r)^2 = 4, t + mean - sqrt(4 / k - variance), is exact once {S > t} is the
+//   support; otherwise its error is that of the few scores between t and the root: (e / d)^3 / 6 where they
+//   lie dense, (e / d)^2 / 2 where one does.
+// So the closed form where it lies above the bound, and the bound where not, or from pass CLOSED on.  Settled
+// when the step shows that what is left is about 1e-5 d at most, and 1e-7 d as a rule.
+constexpr float STEP_CLOSED = 5e-3f, STEP_NEWTON = 1e-3f;
+constexpr int CLOSED = 8, MOST_PASSES = 40;
+struct Threshold {
+    float t, lo;
+    bool settled;
+    __device__ __forceinline__ void start(float t0) {
+        t = lo = t0;
+        settled = false;
+    }
+    __device__ __forceinline__ void step(float k, float s1, float s2, int pass) {
+        if (!(k > 0.f)) {  // above all scores: back to the bound
+            settled = !(t > lo);
+            t = lo;
+            return;
+        }
+        lo = fmaxf(lo, t + (s2 - 4.f) / (2.f * s1));
+        const float mean = s1 / k, rest = 4.f / k - (s2 / k - mean * mean);
+        const float root = t + mean - sqrtf(fmaxf(rest, 0.f));
+        const bool closed = rest >= 0.f && root >= lo && pass <= CLOSED;
+        const float next = closed ? root : lo;
+        settled = !(fabsf(next - t) > (closed ? STEP_CLOSED : STEP_NEWTON) * (s2 / s1));
+        t = next;
+    }
+};
+
+// Softmax: one pass over the blocks.  1.5-entmax: a pass for the largest scores (the exact threshold of the four
+// largest maxima of 32-key chunks is the first bound), passes that sum over the scores above t until every
+// row of both tiles has settled (three as a rule), and the pass that forms P and P V.  S is formed anew in each: the
+// tensor core does it in a third of the time that the sums take, and no row is ever too dense for a list.
+template <bool kSoftmax, bool kF32>
 __global__ void __launch_bounds__(PROMPT_THREADS, 1)
-prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                      const __grid_constant__ CUtensorMap map_v, const AttnArgs a, const FwdOut out, long long first_item) {
+prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v, const AttnArgs a, const FwdOut out, long long first_item) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem + O_Q;
@@ -226,7 +289,7 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             mbar_init(smem_u32(&ctl->q_full[b]), 1);
             mbar_init(smem_u32(&ctl->q_empty[b]), 1);
             mbar_init(smem_u32(&ctl->s_full[b]), 1);
-            mbar_init(smem_u32(&ctl->p_ready[b]), 4);
+            mbar_init(smem_u32(&ctl->s_done[b]), 4);
             mbar_init(smem_u32(&ctl->o_full[b]), 1);
             mbar_init(smem_u32(&ctl->o_empty[b]), 4);
         }
@@ -234,9 +297,11 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             mbar_init(smem_u32(&ctl->k_full[s]), 1);
             mbar_init(smem_u32(&ctl->v_full[s]), 1);
             mbar_init(smem_u32(&ctl->kv_empty[s]), 1);
+            mbar_init(smem_u32(&ctl->voted[s]), 8);
         }
         ctl->abort_flag = 0;
-        ctl->n_q = ctl->n_kv = 0;
+        ctl->n_q = 0;
+        for (int s = 0; s < NS; ++s) ctl->n_k[s] = ctl->n_v[s] = 0;
         ctl->last_bar = ctl->last_par = 0;
         fence_barrier_init();
         prefetch_tmap(&map_q);
@@ -255,15 +320,25 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     const uint32_t tmem = ctl->tmem_base;
     const int items = ctl->items;
 
+    // Whether the pass after vote n is the last one (every row settled), as all roles learn it.
+    auto last_pass = [&](int n, bool& ok) -> bool {
+        ok = wait_bounded(smem_u32(&ctl->voted[n & 3]), (uint32_t)(n >> 2) & 1u, &ctl->abort_flag, wc);
+        return *reinterpret_cast<const volatile uint64_t*>(ctl->vote[n & 3]) == 0;
+    };
+
     if (warp >= W_LOAD) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
-    if (warp == W_LOAD) {
-        if (lane == 0) {
-            int n_kv = 0, n_q = 0;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_OTHER));
+        if (warp == W_LOAD && lane == 0) {
+            int n_kv = 0, n_q = 0, n_vote = 0;
             bool ok = true;
+            auto load_v = [&](int kvh, int row, int st) {
+                mbar_arrive_expect_tx(smem_u32(&ctl->v_full[st]), BLOCK16);
+                tma_load_3d(smem_u32(ring + st * 2 * BLOCK16 + BLOCK16), &map_v, 0, kvh, row, smem_u32(&ctl->v_full[st]));
+                ++ctl->n_v[st];
+            };
             for (int q = 0; q < items && ok; ++q) {
                 const Item it = list[q];
-                const int nb0 = tile_blocks(it, 0), nb1 = tile_blocks(it, 1), nb = max(nb0, nb1);
+                const int nb1 = tile_blocks(it, 1), nb = max(tile_blocks(it, 0), nb1);
                 if (nb == 0) continue;
                 const int kvh = it.head / (a.H / a.Hkv);
                 const int qb = n_q & 1;
@@ -276,27 +351,39 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     tma_load_3d(smem_u32(sQ + (qb * 2 + 1) * TILE_BYTES), &map_q, 0, it.head, row0 + TILE,
                                 smem_u32(&ctl->q_full[qb]));
                 ctl->n_q = ++n_q;
-                for (int j = 0; j < nb; ++j) {
-                    const int st = n_kv % NS;
-                    ok = wait_bounded(smem_u32(&ctl->kv_empty[st]), ((uint32_t)(n_kv / NS) & 1u) ^ 1u, &ctl->abort_flag, wc);
-                    if (!ok) break;
-                    uint8_t* kb = ring + st * 2 * BLOCK16;
-                    mbar_arrive_expect_tx(smem_u32(&ctl->k_full[st]), BLOCK16);
-                    tma_load_3d(smem_u32(kb), &map_k, 0, kvh, it.first + j * KB, smem_u32(&ctl->k_full[st]));
-                    mbar_arrive_expect_tx(smem_u32(&ctl->v_full[st]), BLOCK16);
-                    tma_load_3d(smem_u32(kb + BLOCK16), &map_v, 0, kvh, it.first + j * KB, smem_u32(&ctl->v_full[st]));
-                    ctl->n_kv = ++n_kv;
+                bool last = kSoftmax;
+                for (int pass = 0; ok; ++pass) {
+                    bool known = kSoftmax || pass < 2;  // a pass for the maxima, then at least one of sums
+                    for (int j = 0; j < nb; ++j) {
+                        const int st = n_kv % NS;
+                        ok = wait_bounded(smem_u32(&ctl->kv_empty[st]), ((uint32_t)(n_kv / NS) & 1u) ^ 1u, &ctl->abort_flag, wc);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(smem_u32(&ctl->k_full[st]), BLOCK16);
+                        tma_load_3d(smem_u32(ring + st * 2 * BLOCK16), &map_k, 0, kvh, it.first + j * KB, smem_u32(&ctl->k_full[st]));
+                        ++ctl->n_k[st];
+                        ++n_kv;
+                        // the first two K blocks of a pass are under way before its kind is known
+                        if (!known && (j == 1 || j == nb - 1)) {
+                            last = last_pass(n_vote++, ok);
+                            if (!ok) break;
+                            known = true;
+                            if (last)
+                                for (int b = 0; b <= j; ++b) load_v(kvh, it.first + b * KB, (n_kv - 1 - j + b) % NS);
+                        } else if (last) {
+                            load_v(kvh, it.first + j * KB, st);
+                        }
+                    }
+                    if (last) break;
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp == W_MMA) {
-        if (lane == 0) {
+        } else if (warp == W_MMA && lane == 0) {
             constexpr uint32_t IDESC_S = umma_idesc_bf16_f32(TILE, KB);
             constexpr uint32_t IDESC_O = umma_idesc_bf16_f32_bmn(TILE, HEAD_DIM);
             uint32_t last_bar = 0, last_par = 0;
-            int n_kv = 0, n_q = 0;
-            int ns[2] = {0, 0}, no[2] = {0, 0};  // score blocks and items of each tile so far
+            int n_kv = 0, n_q = 0, n_vote = 0;
+            uint32_t v_par = 0;                    // bit st: parity of stage st's next V block
+            int ns0 = 0, ns1 = 0, no0 = 0, no1 = 0;  // score blocks and items of each tile so far
+            bool open0 = false, open1 = false;     // a score block is out that s_done has not been seen for
             bool ok = true;
             auto commit = [&](uint64_t* bar, uint32_t par) {
                 tc_commit(smem_u32(bar));
@@ -305,143 +392,254 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
             };
             for (int q = 0; q < items && ok; ++q) {
                 const Item it = list[q];
-                const int nbw[2] = {tile_blocks(it, 0), tile_blocks(it, 1)};
-                const int nb = max(nbw[0], nbw[1]);
+                const int nbw0 = tile_blocks(it, 0), nbw1 = tile_blocks(it, 1);
+                const int nb = max(nbw0, nbw1);
                 if (nb == 0) continue;
                 const int qb = n_q & 1;
                 ok = wait_bounded(smem_u32(&ctl->q_full[qb]), (uint32_t)(n_q >> 1) & 1u, &ctl->abort_flag, wc);
                 if (!ok) break;
-                // step j: P V of block j - 1, then S of block j, for one tile after the other
-                for (int j = 0; j <= nb && ok; ++j) {
-                    const int st = (n_kv + j) % NS, pst = (n_kv + j + NS - 1) % NS;
-                    if (j < nb) ok = wait_bounded(smem_u32(&ctl->k_full[st]), (uint32_t)((n_kv + j) / NS) & 1u, &ctl->abort_flag, wc);
-                    if (ok && j > 0)
-                        ok = wait_bounded(smem_u32(&ctl->v_full[pst]), (uint32_t)((n_kv + j - 1) / NS) & 1u, &ctl->abort_flag, wc);
-                    if (!ok) break;
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t s_tm = tmem + TM_S + 128u * w, o_tm = tmem + TM_O + 64u * w;
-                        if (j > 0 && j <= nbw[w]) {
-                            if (j == 1)  // O of the item before is read
-                                ok = ok && wait_bounded(smem_u32(&ctl->o_empty[w]), ((uint32_t)no[w] & 1u) ^ 1u, &ctl->abort_flag, wc);
-                            ok = ok && wait_bounded(smem_u32(&ctl->p_ready[w]), (uint32_t)(ns[w] - 1) & 1u, &ctl->abort_flag, wc);
-                            if (!ok) break;
+                bool last = kSoftmax;
+                for (int pass = 0; ok; ++pass) {
+                    // step j: P V of block j - 1 (last pass), then S of block j, for one tile after the other
+                    for (int j = 0; j <= nb && ok; ++j) {
+                        const int st = (n_kv + j) % NS, pst = (n_kv + j + NS - 1) % NS;
+                        if (j == 1 && !kSoftmax && pass >= 2) last = last_pass(n_vote++, ok);
+                        if (ok && j < nb)
+                            ok = wait_bounded(smem_u32(&ctl->k_full[st]), (uint32_t)((n_kv + j) / NS) & 1u, &ctl->abort_flag, wc);
+                        if (ok && j > 0 && last) {
+                            ok = wait_bounded(smem_u32(&ctl->v_full[pst]), (v_par >> pst) & 1u, &ctl->abort_flag, wc);
+                            v_par ^= 1u << pst;
+                        }
+                        if (!ok) break;
+                        auto tile = [&](const int w, const int nbw, int& ns, int& no, bool& open) -> bool {
+                            const uint32_t s_tm = tmem + TM_S + 128u * w, o_tm = tmem + TM_O + 64u * w;
+                            const bool pv = last && j > 0 && j <= nbw;
+                            if (!pv && j >= nbw) return true;
+                            if (open) {  // its softmax is through with the block before
+                                if (!wait_bounded(smem_u32(&ctl->s_done[w]), (uint32_t)(ns - 1) & 1u, &ctl->abort_flag, wc)) return false;
+                                open = false;
+                            }
+                            if (pv && j == 1 &&  // O of the item before is read
+                                !wait_bounded(smem_u32(&ctl->o_empty[w]), ((uint32_t)no & 1u) ^ 1u, &ctl->abort_flag, wc))
+                                return false;
                             tc_fence_after();
-                            const uint64_t vm = umma_desc_mnmajor_sw128(smem_u32(ring + pst * 2 * BLOCK16 + BLOCK16));
-#pragma unroll
-                            for (int k = 0; k < KB / 16; ++k)
-                                tc_mma_bf16_ta(o_tm, s_tm + 8 * k, vm + 128u * k, IDESC_O, (j > 1 || k > 0) ? 1u : 0u);
-                            if (kF32) {
+                            if (pv) {
+                                const uint64_t vm = umma_desc_mnmajor_sw128(smem_u32(ring + pst * 2 * BLOCK16 + BLOCK16));
 #pragma unroll
                                 for (int k = 0; k < KB / 16; ++k)
-                                    tc_mma_bf16_ta(o_tm, s_tm + 64 + 8 * k, vm + 128u * k, IDESC_O, 1u);
+                                    tc_mma_bf16_ta(o_tm, s_tm + 8 * k, vm + 128u * k, IDESC_O, (j > 1 || k > 0) ? 1u : 0u);
+                                if (kF32) {
 #pragma unroll
-                                for (int k = 0; k < KB / 16; ++k)
-                                    tc_mma_bf16_ta(o_tm, tmem + TM_P3 + 64u * w + 8 * k, vm + 128u * k, IDESC_O, 1u);
-                            }
-                            if (j == nbw[w]) {
-                                commit(&ctl->o_full[w], (uint32_t)no[w] & 1u);
-                                ++no[w];
-                            }
-                        }
-                        if (j < nbw[w]) {
-                            tc_fence_after();
-                            const uint64_t dq = umma_desc_kmajor_sw128(smem_u32(sQ + (qb * 2 + w) * TILE_BYTES));
-                            const uint64_t dk = umma_desc_kmajor_sw128(smem_u32(ring + st * 2 * BLOCK16));
+                                    for (int k = 0; k < KB / 16; ++k)
+                                        tc_mma_bf16_ta(o_tm, s_tm + 64 + 8 * k, vm + 128u * k, IDESC_O, 1u);
 #pragma unroll
-                            for (int k = 0; k < HEAD_DIM / 16; ++k) tc_mma_bf16(s_tm, dq + 2u * k, dk + 2u * k, IDESC_S, k > 0 ? 1u : 0u);
-                            commit(&ctl->s_full[w], (uint32_t)ns[w] & 1u);
-                            ++ns[w];
-                        }
+                                    for (int k = 0; k < KB / 16; ++k)
+                                        tc_mma_bf16_ta(o_tm, tmem + TM_P3 + 64u * w + 8 * k, vm + 128u * k, IDESC_O, 1u);
+                                }
+                                if (j == nbw) {
+                                    commit(&ctl->o_full[w], (uint32_t)no & 1u);
+                                    ++no;
+                                }
+                            }
+                            if (j < nbw) {
+                                const uint64_t dq = umma_desc_kmajor_sw128(smem_u32(sQ + (qb * 2 + w) * TILE_BYTES));
+                                const uint64_t dk = umma_desc_kmajor_sw128(smem_u32(ring + st * 2 * BLOCK16));
+#pragma unroll
+                                for (int k = 0; k < HEAD_DIM / 16; ++k)
+                                    tc_mma_bf16(s_tm, dq + 2u * k, dk + 2u * k, IDESC_S, k > 0 ? 1u : 0u);
+                                commit(&ctl->s_full[w], (uint32_t)ns & 1u);
+                                ++ns;
+                                open = true;
+                            }
+                            return true;
+                        };
+                        ok = tile(0, nbw0, ns0, no0, open0) && tile(1, nbw1, ns1, no1, open1);
+                        if (!ok) break;
+                        if (j > 0) commit(&ctl->kv_empty[pst], (uint32_t)((n_kv + j - 1) / NS) & 1u);
                     }
                     if (!ok) break;
-                    if (j > 0) commit(&ctl->kv_empty[pst], (uint32_t)((n_kv + j - 1) / NS) & 1u);
+                    n_kv += nb;
+                    if (last) break;
                 }
                 if (!ok) break;
                 commit(&ctl->q_empty[qb], (uint32_t)(n_q >> 1) & 1u);
-                n_kv += nb;
                 ++n_q;
             }
             ctl->last_bar = last_bar;
             ctl->last_par = last_par;
         }
         __syncwarp();
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_SOFTMAX));
-        // softmax of tile w: thread <-> row r of the tile <-> TMEM lane
+        // tile w: thread <-> row r of the tile <-> TMEM lane
         const int w = warp >> 2, r = tid & (TILE - 1);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lanes + TM_S + 128u * w, o_tm = tmem + lanes + TM_O + 64u * w;
         const float c = a.scale * LOG2E_F, raise = RAISE / c;
-        const uint64_t c2 = f2pack(c, c);
-        int ns = 0, no = 0, n_kv = 0;
+        const uint64_t scale2 = f2pack(a.scale, a.scale);
+        int ns = 0, no = 0, n_kv = 0, n_vote = 0;
+        uint32_t v_par = 0;  // bit st: parity of stage st's next V block
         bool live = true;
+        auto wait = [&](uint64_t* bar, uint32_t par) {
+            live = __all_sync(0xffffffffu, wait_bounded(smem_u32(bar), par, &ctl->abort_flag, wc));
+            return live;
+        };
+        auto arrive = [&](uint64_t* bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(bar));
+        };
+        // the scores of the tile's next block, keys behind the row at -inf in its last one
+        auto scores = [&](float (&v)[4][32], bool diag) -> bool {
+            if (!wait(&ctl->s_full[w], (uint32_t)ns & 1u)) return false;
+            ++ns;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_ld32(s_tm + 32 * k, v[k]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tmem_wait_ld(v[k]);
+            if (diag)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * k + e > r) v[k][e] = -INFINITY;
+            return true;
+        };
         for (int q = 0; q < items && live; ++q) {
             const Item it = list[q];
             const int nb = tile_blocks(it, w), nb_all = max(tile_blocks(it, 0), tile_blocks(it, 1));
+            if (nb_all == 0) continue;
             const int i = (2 * it.pair + w) * TILE + r;
-            float m = -INFINITY;
-            uint64_t l2 = 0, l3 = 0;
-            for (int j = 0; j < nb; ++j) {
-                live = __all_sync(0xffffffffu, wait_bounded(smem_u32(&ctl->s_full[w]), (uint32_t)ns & 1u, &ctl->abort_flag, wc));
-                if (!live) break;
-                ++ns;
-                tc_fence_after();
-                float v[4][32];
+            Threshold th{0.f, 0.f, true};
+            bool odd = false;  // 1.5-entmax: infinite or NaN scores
+            if (!kSoftmax) {
+                float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
+                for (int j = 0; j < nb; ++j) {
+                    float v[4][32];
+                    if (!scores(v, j == nb - 1)) break;
+                    arrive(&ctl->s_done[w]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_ld32(s_tm + 32 * k, v[k]);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) tmem_wait_ld(v[k]);
-                const bool diag = j == nb - 1;
-                if (diag) {  // keys behind the row
-                    const int lim = i - j * KB;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * k + e > lim) v[k][e] = -INFINITY;
-                }
-                const float top = fmaxf(fmaxf(max32(v[0]), max32(v[1])), fmaxf(max32(v[2]), max32(v[3])));
-                if (j == 0) {
-                    m = top == -INFINITY ? 0.f : top;  // -inf: infinite inputs only (key 0 is every row's)
-                } else if (__any_sync(0xffffffffu, top > m + raise)) {
-                    // O and l to the new reference, row by row (a row's numbers do not depend on its neighbours).  S
-                    // of this block was issued behind P V of the last, so O is at rest
-                    const float n = top > m + raise ? top : m, f = ex2((m - n) * c);
-                    m = n;
-                    const uint64_t f2 = f2pack(f, f);
-                    l2 = f2mul(l2, f2);
-                    l3 = f2mul(l3, f2);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float o[32];
-                        uint32_t u[32];
-                        tmem_ld32(o_tm + 32 * k, o);
-                        tmem_wait_ld(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
-                        tmem_st32(o_tm + 32 * k, u);
+                    for (int k = 0; k < 4; ++k) {
+                        const float cm = max32_nan(v[k]);
+                        odd |= cm != cm;
+                        a3 = fmaxf(a3, fminf(a2, cm));
+                        a2 = fmaxf(a2, fminf(a1, cm));
+                        a1 = fmaxf(a1, fminf(a0, cm));
+                        a0 = fmaxf(a0, cm);
                     }
                 }
-                const float off = -m * c;
-                const uint64_t off2 = f2pack(off, off);
+                n_kv += nb_all;
+                a0 *= a.scale;
+                th.start(fmaxf(a0 - 2.f, top4_bound<true>(a0, a1 * a.scale, a2 * a.scale, a3 * a.scale, 4.f)));
+                odd |= !(fabsf(a0) < INFINITY);
+                if (odd || i >= it.len) {
+                    th.start(0.f);
+                    th.settled = true;
+                }
+                bool more = true;
+                for (int pass = 1; more && live; ++pass) {
+                    const uint64_t t2 = f2pack(-th.t, -th.t);
+                    uint64_t k2 = 0, s1 = 0, s2 = 0, s3 = 0, s4 = 0;
+                    for (int j = 0; j < nb; ++j) {
+                        float v[4][32];
+                        if (!scores(v, j == nb - 1)) break;
+                        arrive(&ctl->s_done[w]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const uint64_t d = f2relu(f2fma(f2pack(v[k][e], v[k][e + 1]), scale2, t2));
+                                float x, y;
+                                f2unpack(d, x, y);
+                                k2 = f2add(k2, f2pack(above0(x), above0(y)));
+                                if (e & 2) {
+                                    s1 = f2add(s1, d);
+                                    s2 = f2fma(d, d, s2);
+                                } else {
+                                    s3 = f2add(s3, d);
+                                    s4 = f2fma(d, d, s4);
+                                }
+                            }
+                    }
+                    n_kv += nb_all;
+                    if (!live) break;
+                    if (i < it.len && !th.settled) {
+                        float kx, ky, x0, x1, y0, y1;
+                        f2unpack(k2, kx, ky);
+                        f2unpack(f2add(s1, s3), x0, x1);
+                        f2unpack(f2add(s2, s4), y0, y1);
+                        th.step(kx + ky, x0 + x1, y0 + y1, pass);
+                    }
+                    const bool any = __any_sync(0xffffffffu, !th.settled && pass < MOST_PASSES);
+                    if (lane == 0) {
+                        ctl->vote[n_vote & 3][warp] = any;
+                        mbar_arrive(smem_u32(&ctl->voted[n_vote & 3]));
+                    }
+                    bool ok;
+                    more = !last_pass(n_vote++, ok);
+                    live = __all_sync(0xffffffffu, ok);
+                }
+            }
+            if (!live) break;
+            // the pass that forms P: softmax weights on the way to the running reference m, or 1.5-entmax weights
+            // at the threshold found
+            float m = -INFINITY;
+            uint64_t l2 = 0, l3 = 0;
+            const float half = 0.5f * a.scale, t_half = -0.5f * th.t;
+            const uint64_t t2 = f2pack(t_half, t_half), h2 = f2pack(half, half), c2 = f2pack(c, c);
+            for (int j = 0; j < nb; ++j) {
+                float v[4][32];
+                const bool diag = j == nb - 1;
+                if (!scores(v, diag)) break;
+                uint64_t off2 = 0;
+                if (kSoftmax) {
+                    const float top = fmaxf(fmaxf(max32(v[0]), max32(v[1])), fmaxf(max32(v[2]), max32(v[3])));
+                    if (j == 0) {
+                        m = top == -INFINITY ? 0.f : top;  // -inf: infinite inputs only (key 0 is every row's)
+                    } else if (__any_sync(0xffffffffu, top > m + raise)) {
+                        // O and l to the new reference, row by row (a row's numbers do not depend on its neighbours).
+                        // S of this block was issued behind P V of the last, so O is at rest
+                        const float n = top > m + raise ? top : m, f = ex2((m - n) * c);
+                        m = n;
+                        const uint64_t f2 = f2pack(f, f);
+                        l2 = f2mul(l2, f2);
+                        l3 = f2mul(l3, f2);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            float o[32];
+                            uint32_t u[32];
+                            tmem_ld32(o_tm + 32 * k, o);
+                            tmem_wait_ld(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                            tmem_st32(o_tm + 32 * k, u);
+                        }
+                    }
+                    const float off = -m * c;
+                    off2 = f2pack(off, off);
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t hi[16], mid[16], lo[16];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const uint64_t x = f2fma(f2pack(v[k][e], v[k][e + 1]), c2, off2);
+                        const uint64_t x = f2pack(v[k][e], v[k][e + 1]);
                         uint64_t p;
-                        if (!kF32 && (e / 2) % (32 / EMULATED) == 0) {
-                            p = f2exp2_poly(x);
+                        if (!kSoftmax) {
+                            p = f2relu(f2fma(x, h2, t2));
+                            p = f2mul(p, p);
+                        } else if (!kF32 && (e / 2) % (32 / EMULATED) == 0) {
+                            p = f2exp2_poly(f2fma(x, c2, off2));
                         } else {
                             float x0, x1;
-                            f2unpack(x, x0, x1);
+                            f2unpack(f2fma(x, c2, off2), x0, x1);
                             p = f2pack(ex2(x0), ex2(x1));
                         }
-                        if (e & 2) l3 = f2add(l3, p);
-                        else l2 = f2add(l2, p);
+                        if (kSoftmax) {
+                            if (e & 2) l3 = f2add(l3, p);
+                            else l2 = f2add(l2, p);
+                        }
                         if (kF32) {
                             f2split3(p, hi[e >> 1], mid[e >> 1], lo[e >> 1]);
                         } else {
@@ -463,9 +661,7 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     const int live_rows = it.len - j * KB;
                     if (live_rows < KB) {
                         const int st = (n_kv + j) % NS;
-                        live = __all_sync(0xffffffffu, wait_bounded(smem_u32(&ctl->v_full[st]), (uint32_t)((n_kv + j) / NS) & 1u,
-                                                                    &ctl->abort_flag, wc));
-                        if (!live) break;
+                        if (!wait(&ctl->v_full[st], ((v_par >> st) ^ (uint32_t)(j / NS)) & 1u)) break;
                         if (r >= live_rows) {
                             uint4* row = reinterpret_cast<uint4*>(ring + st * 2 * BLOCK16 + BLOCK16 + r * 128);
 #pragma unroll
@@ -474,13 +670,14 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                         fence_proxy_async_smem();
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->p_ready[w]));
+                arrive(&ctl->s_done[w]);
             }
+            // nb_all V blocks went through the ring from stage n_kv % NS on
+            if ((nb_all / NS) & 1) v_par ^= (1u << NS) - 1;
+            for (int k = 0; k < nb_all % NS; ++k) v_par ^= 1u << ((n_kv + k) % NS);
+            n_kv += nb_all;
             if (nb > 0 && live) {
-                live = __all_sync(0xffffffffu, wait_bounded(smem_u32(&ctl->o_full[w]), (uint32_t)no & 1u, &ctl->abort_flag, wc));
-                if (!live) break;
+                if (!wait(&ctl->o_full[w], (uint32_t)no & 1u)) break;
                 ++no;
                 tc_fence_after();
                 float o[2][32];
@@ -488,16 +685,18 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                 tmem_ld32(o_tm + 32, o[1]);
                 tmem_wait_ld(o[0]);
                 tmem_wait_ld(o[1]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->o_empty[w]));
-                float x0, x1, x2, x3;
-                f2unpack(l2, x0, x1);
-                f2unpack(l3, x2, x3);
-                const float l = (x0 + x1) + (x2 + x3), inv = 1.f / l;
+                arrive(&ctl->o_empty[w]);
+                float inv = odd ? NAN : 1.f, tau = odd ? NAN : th.t;
+                if (kSoftmax) {
+                    float x0, x1;
+                    f2unpack(f2add(l2, l3), x0, x1);
+                    const float l = x0 + x1;
+                    inv = 1.f / l;
+                    tau = (m * c + log2f(l)) * LN2_F;
+                }
                 if (i < it.len) {
                     const size_t t = (size_t)(it.first + i);
-                    out.tau[(size_t)it.head * a.T + t] = (m * c + log2f(l)) * LN2_F;
+                    out.tau[(size_t)it.head * a.T + t] = tau;
                     const size_t at = (t * a.H + it.head) * HEAD_DIM;
                     if (kF32) {
                         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out.O) + at);
@@ -516,7 +715,6 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
                     }
                 }
             }
-            n_kv += nb_all;
         }
     }
 
@@ -527,9 +725,9 @@ prompt_softmax_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_co
     if (flag_set(&ctl->abort_flag)) {
         if (lane == 0 && warp == W_LOAD) {
             for (int n = max(0, ctl->n_q - 2); n < ctl->n_q; ++n) wait_drain(smem_u32(&ctl->q_full[n & 1]), (uint32_t)(n >> 1) & 1u);
-            for (int n = max(0, ctl->n_kv - NS); n < ctl->n_kv; ++n) {
-                wait_drain(smem_u32(&ctl->k_full[n % NS]), (uint32_t)(n / NS) & 1u);
-                wait_drain(smem_u32(&ctl->v_full[n % NS]), (uint32_t)(n / NS) & 1u);
+            for (int s = 0; s < NS; ++s) {
+                if (ctl->n_k[s]) wait_drain(smem_u32(&ctl->k_full[s]), (uint32_t)(ctl->n_k[s] - 1) & 1u);
+                if (ctl->n_v[s]) wait_drain(smem_u32(&ctl->v_full[s]), (uint32_t)(ctl->n_v[s] - 1) & 1u);
             }
         }
         if (lane == 0 && warp == W_MMA && ctl->last_bar) wait_drain(ctl->last_bar, ctl->last_par);
@@ -546,14 +744,16 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 
 }  // namespace
 
-cudaError_t launch_prompt_softmax(const AttnArgs& a, const FwdOut& o, cudaStream_t stream) {
+cudaError_t launch_prompt(const AttnArgs& a, const FwdOut& o, cudaStream_t stream) {
     CUtensorMap mq, mk, mv;
     cudaError_t e = make_packed_map(&mq, a.Q, a.H, 64ll * a.q_step, a.T, TILE);
     if (e == cudaSuccess) e = make_packed_map(&mk, a.K, a.Hkv, 64ll * a.k_step, a.T, KB);
     if (e == cudaSuccess) e = make_packed_map(&mv, a.V, a.Hkv, 64ll * a.v_step, a.T, KB);
     if (e != cudaSuccess) return e;
-    const auto f = o.out_f32 ? prompt_softmax_kernel<true> : prompt_softmax_kernel<false>;
-    e = ensure_smem_attr(reinterpret_cast<const void*>(f), PROMPT_SMEM, o.out_f32 ? 21 : 22);
+    const bool soft = softmax_alpha(a);
+    const auto f = soft ? (o.out_f32 ? prompt_kernel<true, true> : prompt_kernel<true, false>)
+                        : (o.out_f32 ? prompt_kernel<false, true> : prompt_kernel<false, false>);
+    e = ensure_smem_attr(reinterpret_cast<const void*>(f), PROMPT_SMEM, 20 + 2 * soft + (o.out_f32 != 0));
     if (e != cudaSuccess) return e;
     // at most this many pairs; a CTA lists LIST of them
     const long long most = unit_base(a.T, a.n_seqs, PAIR, PAIR - 1) * a.H;
@@ -582,7 +782,7 @@ extern "C" int entmax_attn_prompt(const void* Q, long long q_stride, const void*
     if (out_dtype != ENTMAX_BF16 && out_dtype != ENTMAX_F32) return ENTMAX_ERR_ARG;
     if (H == 0 || H_kv == 0) return H == H_kv ? ENTMAX_OK : ENTMAX_ERR_ARG;
     if (H % H_kv != 0) return ENTMAX_ERR_ARG;
-    if (n > MAX_SEQS || H > 65535 || max_len > (soft ? MAX_PAIRS * PAIR : MAX_L)) return ENTMAX_ERR_UNSUPPORTED;
+    if (n > MAX_SEQS || H > 65535 || max_len > (soft || alpha == 1.5f ? MAX_PAIRS * PAIR : MAX_L)) return ENTMAX_ERR_UNSUPPORTED;
     if (n == 0 || T == 0 || max_len == 0) return ENTMAX_OK;
     if (!Q || !K || !V || !O || !tau || !cu) return ENTMAX_ERR_ARG;
     if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16) || !aligned(tau, 4) || !aligned(cu, 4))
@@ -605,5 +805,5 @@ extern "C" int entmax_attn_prompt(const void* Q, long long q_stride, const void*
     a.v_step = (int)(v_stride / 64);
     a.arg_status = args_status;
     const FwdOut o{O, out_dtype == ENTMAX_F32, tau, SavedSupport{}, nullptr, nullptr};
-    return abi_record(soft ? launch_prompt_softmax(a, o, stream) : launch_fwd_packed(a, o, stream));
+    return abi_record(generic_alpha(a) && !soft ? launch_fwd_packed(a, o, stream) : launch_prompt(a, o, stream));
 }

@@ -135,12 +135,13 @@ ENTMAX_API size_t entmax_cache_attn_workspace_size(int n, int H, int H_kv, float
  *                them); 16-byte aligned.
  *   cu           device int32 [n + 1], not decreasing, cu[n] <= T: sequence i has the tokens cu[i] .. cu[i+1] - 1.
  *                Tokens outside all sequences are neither read as keys nor written.
- *   max_len      no sequence is longer; at most 16384, for softmax 1048576 (else ENTMAX_ERR_UNSUPPORTED).
- *                A sequence that is longer, or lies outside [0, T], is left out.
+ *   max_len      no sequence is longer; at most 1048576, for alpha other than 1 and 1.5 16384 (else
+ *                ENTMAX_ERR_UNSUPPORTED).  A sequence that is longer, or lies outside [0, T], is left out.
  *   alpha        in [1, 2] as in entmax_attn_fwd_ex (within 1e-4 of 1: softmax).
  *   O            [T][H][64] bf16 or fp32, 16-byte aligned; tau [H][T] fp32.
- * Softmax weights multiply the values as one bf16 number for a bf16 output and as three (24 bits) for
- * an fp32 output.  n <= 4096.  Results are the same bit for bit from run to run.
+ * The weights of softmax and 1.5-entmax multiply the values as one bf16 number for a bf16 output and as
+ * three (24 bits) for an fp32 output.  NaN or infinite scores make their row NaN (alpha 1 and 1.5).
+ * n <= 4096.  Results are the same bit for bit from run to run.
  */
 ENTMAX_API int entmax_attn_prompt(const void* Q, long long q_stride, const void* K, long long k_stride, const void* V,
                                   long long v_stride, const int32_t* cu, int n, int T, int max_len, float scale,

@@ -103,7 +103,7 @@ def prompt(**kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(n=-1), E.ENTMAX_ERR_ARG), (dict(T=-1), E.ENTMAX_ERR_ARG), (dict(max_len=-1), E.ENTMAX_ERR_ARG),
-    (dict(n=4097), E.ENTMAX_ERR_UNSUPPORTED), (dict(max_len=16385), E.ENTMAX_ERR_UNSUPPORTED), (dict(D=128), E.ENTMAX_ERR_UNSUPPORTED),
+    (dict(n=4097), E.ENTMAX_ERR_UNSUPPORTED), (dict(max_len=16385, alpha=1.25), E.ENTMAX_ERR_UNSUPPORTED), (dict(D=128), E.ENTMAX_ERR_UNSUPPORTED),
     (dict(max_len=(1 << 20) + 1, alpha=1.0), E.ENTMAX_ERR_UNSUPPORTED), (dict(H=3), E.ENTMAX_ERR_ARG), (dict(H=0), E.ENTMAX_ERR_ARG),
     (dict(H=0, Hkv=0), E.ENTMAX_OK), (dict(n=0), E.ENTMAX_OK), (dict(T=0), E.ENTMAX_OK), (dict(alpha=2.01), E.ENTMAX_ERR_ARG),
     (dict(alpha=float("nan")), E.ENTMAX_ERR_ARG), (dict(scale=float("inf")), E.ENTMAX_ERR_ARG), (dict(out=5), E.ENTMAX_ERR_ARG),

@@ -5,8 +5,11 @@ Tolerances.  Scores are sums of 64 exact products in fp32, scaled once: |dS| <= 
                |dO| <= (2 delta + 2^-20) sum p |V|.
   softmax, bf16 output:  2 delta + 2^-8 (one bf16 part, half a step) + 2^-18 (exponentials from a polynomial: 2.8e-6),
                then the output's own rounding, 2^-8 |O|.   |dtau| <= delta + 2^-18 (1 + |tau|) for both.
-  1.5-entmax and other alpha: the suite's flat bounds (gpu_helpers): 1e-2 on the fp32 output, 1e-3 on tau; the bf16
-               output is the fp32 output rounded.
+  1.5-entmax:  tau moves by at most delta, plus what the solver leaves: 1.3e-5 of the support's mean depth (at most 2)
+               and 2^-22 of the scores' size; with e the sum of both and of delta, |dp| <= e (sqrt p + e) for the keys
+               near or in the support, 2^-20 p for the sums; the bf16 output adds 2^-8 of each weight and of itself.
+  other alpha: the suite's flat bounds (gpu_helpers): 1e-2 on the fp32 output, 1e-3 on tau; the bf16 output is the
+               fp32 output rounded.
 """
 import random
 
@@ -38,13 +41,15 @@ def starts(lens):
 
 
 def reference(Q, K, V, lens, scale, alpha, first=0):
-    """fp64 O [T, H, 64], tau [H, T], sum p |V| and max |S| by row (numpy), for the rows of the sequences."""
+    """fp64 O [T, H, 64], tau [H, T], sum p |V|, max |S| by row, and for 1.5-entmax sum sqrt(p) |V| over keys near or in
+    the support and sum |V| over them (numpy), for the rows of the sequences."""
     from oracle import oracle as orc
     q, k, v = (t.double().cpu().numpy() for t in (Q, K, V))
     T, H = q.shape[:2]
     G = H // k.shape[1]
     O, tau = np.zeros((T, H, 64)), np.full((H, T), np.inf)
     A, M = np.zeros((T, H, 64)), np.zeros((H, T))
+    B, C = np.zeros((T, H, 64)), np.zeros((T, H, 64))
     at = first
     for n in lens:
         for h in range(H):
@@ -58,6 +63,7 @@ def reference(Q, K, V, lens, scale, alpha, first=0):
                 tau[h, at:at + n] = t[:, 0]
                 O[at:at + n, h] = P @ V_
                 A[at:at + n, h] = P @ np.abs(V_)
+            if n:
                 M[h, at:at + n] = np.abs(np.where(np.isinf(S), 0, S)).max(1)
         at += n
     if alpha != 1.0:
@@ -69,13 +75,20 @@ def reference(Q, K, V, lens, scale, alpha, first=0):
                 o, t = orc.attn_fwd(one(q), one(rep(k)), one(rep(v)), None, True, 0, scale, alpha=alpha)
                 O[at:at + n] = o[0].transpose(1, 0, 2)
                 tau[:, at:at + n] = t[0]
+                for h in range(H if alpha == 1.5 else 0):
+                    S = scale * (q[at:at + n, h] @ k[at:at + n, h // G].T)
+                    S[np.triu_indices(n, 1)] = -np.inf
+                    w = np.maximum(0, (S - t[0][h][:, None]) / 2)
+                    V_ = np.abs(v[at:at + n, h // G])
+                    A[at:at + n, h], B[at:at + n, h] = (w * w) @ V_, w @ V_
+                    C[at:at + n, h] = (S > t[0][h][:, None] - 1e-2) @ V_
             at += n
-    return O, tau, A, M
+    return O, tau, A, M, B, C
 
 
 def check(Q, K, V, lens, out, scale, alpha, first=0):
     (O32, tau32), (O16, tau16) = out
-    O, tau, A, M = reference(Q, K, V, lens, scale, alpha, first)
+    O, tau, A, M, B, C = reference(Q, K, V, lens, scale, alpha, first)
     rows = slice(first, first + sum(lens))
     o32, o16, t32, t16 = (x.double().cpu().numpy() for x in (O32, O16, tau32, tau16))
     if alpha == 1.0:
@@ -84,6 +97,15 @@ def check(Q, K, V, lens, out, scale, alpha, first=0):
         assert (np.abs(o16 - O)[rows] <= (2 * delta + 2.0 ** -8 + 2.0 ** -18) * A[rows] * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(O[rows])).all()
         for t in (t32, t16):
             assert (np.abs(t - tau)[:, rows] <= delta[:, :, 0].T + 2.0 ** -18 * (1 + np.abs(tau[:, rows]))).all()
+    elif alpha == 1.5:
+        delta = 2.0 ** -18 * (1 + M.T[rows, :, None])
+        left = delta + 2.6e-5 + 2.0 ** -22 * M.T[rows, :, None]
+        for t in (t32, t16):
+            assert (np.abs(t - tau)[:, rows] <= left[:, :, 0].T).all(), (np.abs(t - tau)[:, rows] / left[:, :, 0].T).max()
+        e = delta + left
+        room = e * (B[rows] + e * C[rows]) + 2.0 ** -20 * A[rows]
+        assert (np.abs(o32 - O)[rows] <= room).all(), np.abs(o32 - O)[rows].max()
+        assert (np.abs(o16 - O)[rows] <= (room + 2.0 ** -8 * A[rows]) * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(O[rows])).all()
     else:
         assert np.abs(o32 - O)[rows].max() <= O_TOL and np.abs(t32 - tau)[:, rows].max() <= TAU_TOL
         assert_bf16_is_rounded(O16[rows], O32[rows])
@@ -220,20 +242,38 @@ def test_same_bits_streams_and_graphs(alpha):
     assert torch.equal(O3[:1000], O4[:1000]) and torch.equal(tau3[:, :1000], tau4[:, :1000])
 
 
-def test_wait_bound(alpha=1.0):
-    """A 1 ns bound makes the softmax kernel's waits give up: reported, and the next call is right."""
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_wait_bound(alpha):
+    """A 1 ns bound makes the kernel's waits give up: reported, and the next call is right."""
     import entmax_tcgen05_tma_b200 as E
     Q, K, V = inputs(3000, 8, 2, 12)
     cu = [0, 1000, 3000]
     E.entmax_attn_set_wait_timeout_ns(1)
     try:
-        both(Q, K, V, cu, 2000, scale=0.125, alpha=1.0)
+        both(Q, K, V, cu, 2000, scale=0.125, alpha=alpha)
         assert E.entmax_attn_device_status() == E.ENTMAX_ERR_TIMEOUT
     finally:
         E.entmax_attn_set_wait_timeout_ns(0)
     check(Q[:, :2], K[:, :1], V[:, :1], [1000, 2000],
-          [(O[:, :2], t[:2]) for O, t in both(Q, K, V, cu, 2000, scale=0.125, alpha=1.0)], 0.125, 1.0)
+          [(O[:, :2], t[:2]) for O, t in both(Q, K, V, cu, 2000, scale=0.125, alpha=alpha)], 0.125, alpha)
     assert E.entmax_attn_device_status() == 0
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_not_finite(alpha):
+    """A NaN or infinite token makes the rows that read it NaN, and no row before it or of another sequence."""
+    for bad in (float("nan"), float("inf")):
+        Q, K, V = inputs(500, 2, 1, 15)
+        clean = both(Q, K, V, [0, 300, 500], 300, scale=0.125, alpha=alpha)
+        K[100, 0, 7] = bad
+        for (O, tau), (P, t) in zip(both(Q, K, V, [0, 300, 500], 300, scale=0.125, alpha=alpha), clean):
+            if bad != bad:
+                assert torch.isnan(O[100:300]).all() and torch.isnan(tau[:, 100:300]).all()
+            else:  # +inf for some queries, -inf for others
+                odd = torch.isnan(tau[:, 100:300]) | torch.isinf(tau[:, 100:300])
+                assert odd.any()
+            for rows in (slice(0, 100), slice(300, 500)):
+                assert torch.equal(O[rows], P[rows]) and torch.equal(tau[:, rows], t[:, rows])
 
 
 def test_equals_the_dense_forward():
@@ -253,8 +293,8 @@ def test_refusals():
     Q, K, V = inputs(100, 4, 2, 14)
     cu = ints([0, 100])
     for kw, code in ((dict(alpha=2.5), E.ENTMAX_ERR_ARG), (dict(alpha=0.5), E.ENTMAX_ERR_ARG), (dict(scale=0.0), E.ENTMAX_ERR_ARG),
-                     (dict(max_len=-1), E.ENTMAX_ERR_ARG), (dict(max_len=16385), E.ENTMAX_ERR_UNSUPPORTED),
-                     (dict(max_len=(1 << 20) + 1, alpha=1.0), E.ENTMAX_ERR_UNSUPPORTED)):
+                     (dict(max_len=-1), E.ENTMAX_ERR_ARG), (dict(max_len=16385, alpha=1.4), E.ENTMAX_ERR_UNSUPPORTED),
+                     (dict(max_len=(1 << 20) + 1, alpha=1.5), E.ENTMAX_ERR_UNSUPPORTED)):
         a = dict(max_len=100)
         a.update(kw)
         with pytest.raises(E.EntmaxError) as e:
