@@ -34,7 +34,7 @@ constexpr int KB = 128;                      // keys of a block
 constexpr int PAIR = 2 * TILE;               // rows of a work item
 constexpr int NS = 4;                        // ring stages, a K and a V block each
 constexpr int BLOCK16 = KB * HEAD_DIM * 2;   // 16 KiB
-constexpr int W_LOAD = 8, W_MMA = 9, PROMPT_THREADS = 384;  // warps 10 and 11 only complete a warpgroup
+constexpr int W_LOAD = 8, W_MMA = 9, PROMPT_THREADS = 384;  // warps 9 and 10: MMA; 11 only completes a warpgroup
 // registers a thread: 168 at launch (384 threads), then 216 for the two softmax warpgroups, which hold a row's
 // 128 scores, and 72 for the third: 216 + 216 + 72 = 3 * 168
 constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
@@ -56,7 +56,8 @@ struct Ctl {
     uint64_t q_full[2], q_empty[2];
     uint64_t k_full[NS], v_full[NS], kv_empty[NS];
     uint64_t s_full[2];            // S of tile w is in TMEM
-    uint64_t s_done[2];            // its warps have read it and, in a last pass, stored P
+    uint64_t s_read[2];            // its warps have it in registers (where P lies over S: have stored P)
+    uint64_t p_full[2], p_empty[2];  // P of tile w stored; P V formed from it
     uint64_t o_full[2], o_empty[2];
     uint64_t voted[NS];            // the eight warps' votes on whether another pass of sums is needed
     uint8_t vote[NS][8];
@@ -64,15 +65,15 @@ struct Ctl {
     int abort_flag;
     int items;
     int n_q, n_k[NS], n_v[NS];     // loads issued
-    uint32_t last_bar, last_par;   // the MMA thread's last commit
+    uint32_t last_bar[2], last_par[2];  // the MMA warps' last commits
 };
 constexpr int PROMPT_SMEM = O_CTL + (int)sizeof(Ctl) + 1024;
 static_assert(PROMPT_SMEM <= 227 * 1024, "shared memory");
 // while the work list is made, the ring holds the sequences' pair counts and the counts by size
 static_assert((MAX_SEQS + 3 * (MAX_PAIRS + 2)) * 4 <= NS * 2 * BLOCK16, "list scratch");
-// TMEM columns: S of tile w at 128 w, O at 256 + 64 w.  P~ lies over S: its bf16 pairs in columns 0 .. 63 of it, a
-// second part in 64 .. 127; a third has columns of its own.
-constexpr int TM_S = 0, TM_O = 256, TM_P3 = 384;
+// TMEM columns: S of tile w at 128 w, O at 256 + 64 w, P at 384 + 64 w, so that S of the next block is formed while
+// this block's P is.  Three parts do not fit beside S: the first two then lie over S, and the third at P's place.
+constexpr int TM_S = 0, TM_O = 256, TM_P = 384;
 
 // Blocks of tile w of a pair: its last block holds the diagonal.
 __device__ __forceinline__ int tile_blocks(const Item& it, int w) {
@@ -287,22 +288,24 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (tid == 0) {
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_u32(&ctl->q_full[b]), 1);
-            mbar_init(smem_u32(&ctl->q_empty[b]), 1);
+            mbar_init(smem_u32(&ctl->q_empty[b]), 2);
             mbar_init(smem_u32(&ctl->s_full[b]), 1);
-            mbar_init(smem_u32(&ctl->s_done[b]), 4);
+            mbar_init(smem_u32(&ctl->s_read[b]), 4);
+            mbar_init(smem_u32(&ctl->p_full[b]), 4);
+            mbar_init(smem_u32(&ctl->p_empty[b]), 1);
+            ctl->last_bar[b] = ctl->last_par[b] = 0;
             mbar_init(smem_u32(&ctl->o_full[b]), 1);
             mbar_init(smem_u32(&ctl->o_empty[b]), 4);
         }
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&ctl->k_full[s]), 1);
             mbar_init(smem_u32(&ctl->v_full[s]), 1);
-            mbar_init(smem_u32(&ctl->kv_empty[s]), 1);
+            mbar_init(smem_u32(&ctl->kv_empty[s]), 2);
             mbar_init(smem_u32(&ctl->voted[s]), 8);
         }
         ctl->abort_flag = 0;
         ctl->n_q = 0;
         for (int s = 0; s < NS; ++s) ctl->n_k[s] = ctl->n_v[s] = 0;
-        ctl->last_bar = ctl->last_par = 0;
         fence_barrier_init();
         prefetch_tmap(&map_q);
         prefetch_tmap(&map_k);
@@ -376,97 +379,115 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     if (last) break;
                 }
             }
-        } else if (warp == W_MMA && lane == 0) {
+        } else if (warp == W_MMA || warp == W_MMA + 1) {
+            // A warp per tile.  The whole warp runs the loops, so that addresses and descriptors stay in uniform
+            // registers, and one elected lane issues (issued from a branch of lane 0 alone, each product took
+            // about 130 clocks and the issue bounded the kernel).
+            const bool leader = elect_one();
+            const int w = warp - W_MMA;
             constexpr uint32_t IDESC_S = umma_idesc_bf16_f32(TILE, KB);
             constexpr uint32_t IDESC_O = umma_idesc_bf16_f32_bmn(TILE, HEAD_DIM);
             uint32_t last_bar = 0, last_par = 0;
-            int n_kv = 0, n_q = 0, n_vote = 0;
-            uint32_t v_par = 0;                    // bit st: parity of stage st's next V block
-            int ns0 = 0, ns1 = 0, no0 = 0, no1 = 0;  // score blocks and items of each tile so far
-            bool open0 = false, open1 = false;     // a score block is out that s_done has not been seen for
+            int n_kv = 0, n_q = 0, n_vote = 0, ns = 0, np = 0, no = 0;  // ns, np, no: blocks S, blocks P V, items so far
+            uint32_t v_par = 0;  // bit st: parity of stage st's next V block
             bool ok = true;
             auto commit = [&](uint64_t* bar, uint32_t par) {
-                tc_commit(smem_u32(bar));
+                if (leader) tc_commit(smem_u32(bar));
                 last_bar = smem_u32(bar);
                 last_par = par;
             };
-            for (int q = 0; q < items && ok; ++q) {
+            auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
+                return __all_sync(0xffffffffu, wait_bounded(smem_u32(bar), par, &ctl->abort_flag, wc));
+            };
+            const uint32_t ring_u = __shfl_sync(0xffffffffu, smem_u32(ring), 0);
+            const uint32_t q_u = __shfl_sync(0xffffffffu, smem_u32(sQ), 0) + w * TILE_BYTES;
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t s_tm = tm + TM_S + 128u * w, o_tm = tm + TM_O + 64u * w, p_tm = kF32 ? s_tm : tm + TM_P + 64u * w;
+            const int n_items = __shfl_sync(0xffffffffu, items, 0);
+            for (int q = 0; q < n_items && ok; ++q) {
                 const Item it = list[q];
-                const int nbw0 = tile_blocks(it, 0), nbw1 = tile_blocks(it, 1);
-                const int nb = max(nbw0, nbw1);
+                const int nb_w = __shfl_sync(0xffffffffu, tile_blocks(it, w), 0);
+                const int nb = max(nb_w, __shfl_sync(0xffffffffu, tile_blocks(it, w ^ 1), 0));
                 if (nb == 0) continue;
                 const int qb = n_q & 1;
-                ok = wait_bounded(smem_u32(&ctl->q_full[qb]), (uint32_t)(n_q >> 1) & 1u, &ctl->abort_flag, wc);
-                if (!ok) break;
+                ok = wait(&ctl->q_full[qb], (uint32_t)(n_q >> 1) & 1u);
                 bool last = kSoftmax;
                 for (int pass = 0; ok; ++pass) {
-                    // step j: P V of block j - 1 (last pass), then S of block j, for one tile after the other
+                    // step j: S of block j, and in the last pass P V of block j - 1 (before it where P lies over S)
                     for (int j = 0; j <= nb && ok; ++j) {
                         const int st = (n_kv + j) % NS, pst = (n_kv + j + NS - 1) % NS;
-                        if (j == 1 && !kSoftmax && pass >= 2) last = last_pass(n_vote++, ok);
-                        if (ok && j < nb)
-                            ok = wait_bounded(smem_u32(&ctl->k_full[st]), (uint32_t)((n_kv + j) / NS) & 1u, &ctl->abort_flag, wc);
-                        if (ok && j > 0 && last) {
-                            ok = wait_bounded(smem_u32(&ctl->v_full[pst]), (v_par >> pst) & 1u, &ctl->abort_flag, wc);
-                            v_par ^= 1u << pst;
+                        if (j == 1 && !kSoftmax && pass >= 2) {
+                            last = __all_sync(0xffffffffu, last_pass(n_vote++, ok));
+                            ok = __all_sync(0xffffffffu, ok);
                         }
-                        if (!ok) break;
-                        auto tile = [&](const int w, const int nbw, int& ns, int& no, bool& open) -> bool {
-                            const uint32_t s_tm = tmem + TM_S + 128u * w, o_tm = tmem + TM_O + 64u * w;
-                            const bool pv = last && j > 0 && j <= nbw;
-                            if (!pv && j >= nbw) return true;
-                            if (open) {  // its softmax is through with the block before
-                                if (!wait_bounded(smem_u32(&ctl->s_done[w]), (uint32_t)(ns - 1) & 1u, &ctl->abort_flag, wc)) return false;
-                                open = false;
-                            }
-                            if (pv && j == 1 &&  // O of the item before is read
-                                !wait_bounded(smem_u32(&ctl->o_empty[w]), ((uint32_t)no & 1u) ^ 1u, &ctl->abort_flag, wc))
-                                return false;
+                        // every K block is waited for, used or not: a warp without work would run ahead and release
+                        // a stage twice
+                        if (ok && j < nb) ok = wait(&ctl->k_full[st], (uint32_t)((n_kv + j) / NS) & 1u);
+                        auto form_s = [&]() {
+                            ok = ok && wait(&ctl->s_read[w], ((uint32_t)ns & 1u) ^ 1u);  // the block before is in registers
+                            if (!ok) return;
                             tc_fence_after();
-                            if (pv) {
-                                const uint64_t vm = umma_desc_mnmajor_sw128(smem_u32(ring + pst * 2 * BLOCK16 + BLOCK16));
-#pragma unroll
-                                for (int k = 0; k < KB / 16; ++k)
-                                    tc_mma_bf16_ta(o_tm, s_tm + 8 * k, vm + 128u * k, IDESC_O, (j > 1 || k > 0) ? 1u : 0u);
-                                if (kF32) {
-#pragma unroll
-                                    for (int k = 0; k < KB / 16; ++k)
-                                        tc_mma_bf16_ta(o_tm, s_tm + 64 + 8 * k, vm + 128u * k, IDESC_O, 1u);
-#pragma unroll
-                                    for (int k = 0; k < KB / 16; ++k)
-                                        tc_mma_bf16_ta(o_tm, tmem + TM_P3 + 64u * w + 8 * k, vm + 128u * k, IDESC_O, 1u);
-                                }
-                                if (j == nbw) {
-                                    commit(&ctl->o_full[w], (uint32_t)no & 1u);
-                                    ++no;
-                                }
-                            }
-                            if (j < nbw) {
-                                const uint64_t dq = umma_desc_kmajor_sw128(smem_u32(sQ + (qb * 2 + w) * TILE_BYTES));
-                                const uint64_t dk = umma_desc_kmajor_sw128(smem_u32(ring + st * 2 * BLOCK16));
+                            const uint64_t dq = umma_desc_kmajor_sw128(q_u + qb * 2 * TILE_BYTES);
+                            const uint64_t dk = umma_desc_kmajor_sw128(ring_u + st * 2 * BLOCK16);
+                            if (leader) {
 #pragma unroll
                                 for (int k = 0; k < HEAD_DIM / 16; ++k)
                                     tc_mma_bf16(s_tm, dq + 2u * k, dk + 2u * k, IDESC_S, k > 0 ? 1u : 0u);
-                                commit(&ctl->s_full[w], (uint32_t)ns & 1u);
-                                ++ns;
-                                open = true;
                             }
-                            return true;
+                            commit(&ctl->s_full[w], (uint32_t)ns & 1u);
+                            ++ns;
                         };
-                        ok = tile(0, nbw0, ns0, no0, open0) && tile(1, nbw1, ns1, no1, open1);
+                        auto form_pv = [&]() {
+                            ok = ok && wait(&ctl->v_full[pst], (v_par >> pst) & 1u);
+                            v_par ^= 1u << pst;
+                            if (j > nb_w) return;
+                            if (j == 1) ok = ok && wait(&ctl->o_empty[w], ((uint32_t)no & 1u) ^ 1u);  // O of the item before is read
+                            ok = ok && wait(&ctl->p_full[w], (uint32_t)np & 1u);
+                            if (!ok) return;
+                            tc_fence_after();
+                            const uint64_t vm = umma_desc_mnmajor_sw128(ring_u + pst * 2 * BLOCK16 + BLOCK16);
+                            if (leader) {
+#pragma unroll
+                                for (int k = 0; k < KB / 16; ++k)
+                                    tc_mma_bf16_ta(o_tm, p_tm + 8 * k, vm + 128u * k, IDESC_O, (j > 1 || k > 0) ? 1u : 0u);
+                                if (kF32) {
+#pragma unroll
+                                    for (int k = 0; k < KB / 16; ++k)
+                                        tc_mma_bf16_ta(o_tm, p_tm + 64 + 8 * k, vm + 128u * k, IDESC_O, 1u);
+#pragma unroll
+                                    for (int k = 0; k < KB / 16; ++k)
+                                        tc_mma_bf16_ta(o_tm, tm + TM_P + 64u * w + 8 * k, vm + 128u * k, IDESC_O, 1u);
+                                }
+                            }
+                            commit(&ctl->p_empty[w], (uint32_t)np & 1u);
+                            ++np;
+                            if (j == nb_w) {
+                                commit(&ctl->o_full[w], (uint32_t)no & 1u);
+                                ++no;
+                            }
+                        };
+                        if (kF32) {
+                            if (j > 0 && last) form_pv();
+                            if (j < nb_w) form_s();
+                        } else {
+                            if (j < nb_w) form_s();
+                            if (j > 0 && last) form_pv();
+                        }
                         if (!ok) break;
-                        if (j > 0) commit(&ctl->kv_empty[pst], (uint32_t)((n_kv + j - 1) / NS) & 1u);
+                        if (j > 0 && leader) tc_commit(smem_u32(&ctl->kv_empty[pst]));
                     }
                     if (!ok) break;
                     n_kv += nb;
                     if (last) break;
                 }
                 if (!ok) break;
-                commit(&ctl->q_empty[qb], (uint32_t)(n_q >> 1) & 1u);
+                if (leader) tc_commit(smem_u32(&ctl->q_empty[qb]));
                 ++n_q;
             }
-            ctl->last_bar = last_bar;
-            ctl->last_par = last_par;
+            if (leader) {
+                ctl->last_bar[w] = last_bar;
+                ctl->last_par[w] = last_par;
+            }
         }
         __syncwarp();
     } else {
@@ -475,9 +496,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const int w = warp >> 2, r = tid & (TILE - 1);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lanes + TM_S + 128u * w, o_tm = tmem + lanes + TM_O + 64u * w;
+        const uint32_t p_tm = kF32 ? s_tm : tmem + lanes + TM_P + 64u * w;
         const float c = a.scale * LOG2E_F, raise = RAISE / c;
         const uint64_t scale2 = f2pack(a.scale, a.scale);
-        int ns = 0, no = 0, n_kv = 0, n_vote = 0;
+        int ns = 0, np = 0, no = 0, n_kv = 0, n_vote = 0;
         uint32_t v_par = 0;  // bit st: parity of stage st's next V block
         bool live = true;
         auto wait = [&](uint64_t* bar, uint32_t par) {
@@ -518,7 +540,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 for (int j = 0; j < nb; ++j) {
                     float v[4][32];
                     if (!scores(v, j == nb - 1)) break;
-                    arrive(&ctl->s_done[w]);
+                    arrive(&ctl->s_read[w]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float cm = max32_nan(v[k]);
@@ -544,7 +566,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     for (int j = 0; j < nb; ++j) {
                         float v[4][32];
                         if (!scores(v, j == nb - 1)) break;
-                        arrive(&ctl->s_done[w]);
+                        arrive(&ctl->s_read[w]);
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
@@ -592,14 +614,17 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 float v[4][32];
                 const bool diag = j == nb - 1;
                 if (!scores(v, diag)) break;
+                if (!kF32) arrive(&ctl->s_read[w]);
                 uint64_t off2 = 0;
                 if (kSoftmax) {
                     const float top = fmaxf(fmaxf(max32(v[0]), max32(v[1])), fmaxf(max32(v[2]), max32(v[3])));
                     if (j == 0) {
                         m = top == -INFINITY ? 0.f : top;  // -inf: infinite inputs only (key 0 is every row's)
                     } else if (__any_sync(0xffffffffu, top > m + raise)) {
-                        // O and l to the new reference, row by row (a row's numbers do not depend on its neighbours).
-                        // S of this block was issued behind P V of the last, so O is at rest
+                        // O and l to the new reference, row by row (a row's numbers do not depend on its neighbours),
+                        // once P V of the block before is through
+                        if (!wait(&ctl->p_empty[w], (uint32_t)(np - 1) & 1u)) break;
+                        tc_fence_after();
                         const float n = top > m + raise ? top : m, f = ex2((m - n) * c);
                         m = n;
                         const uint64_t f2 = f2pack(f, f);
@@ -619,6 +644,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     const float off = -m * c;
                     off2 = f2pack(off, off);
                 }
+                // P's columns are free once P V of the block before is through (an item's first block: its O was read)
+                if (!kF32 && j > 0) {
+                    if (!wait(&ctl->p_empty[w], (uint32_t)(np - 1) & 1u)) break;
+                    tc_fence_after();
+                }
+                ++np;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     uint32_t hi[16], mid[16], lo[16];
@@ -648,10 +679,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                             hi[e >> 1] = pack_bf16(x0, x1);
                         }
                     }
-                    tmem_st16(s_tm + 16 * k, hi);
+                    tmem_st16(p_tm + 16 * k, hi);
                     if (kF32) {
-                        tmem_st16(s_tm + 64 + 16 * k, mid);
-                        tmem_st16(tmem + lanes + TM_P3 + 64u * w + 16 * k, lo);
+                        tmem_st16(p_tm + 64 + 16 * k, mid);
+                        tmem_st16(tmem + lanes + TM_P + 64u * w + 16 * k, lo);
                     }
                 }
                 tmem_wait_st();
@@ -670,7 +701,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         fence_proxy_async_smem();
                     }
                 }
-                arrive(&ctl->s_done[w]);
+                arrive(&ctl->p_full[w]);
+                if (kF32 && lane == 0) mbar_arrive(smem_u32(&ctl->s_read[w]));
             }
             // nb_all V blocks went through the ring from stage n_kv % NS on
             if ((nb_all / NS) & 1) v_par ^= (1u << NS) - 1;
@@ -730,7 +762,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 if (ctl->n_v[s]) wait_drain(smem_u32(&ctl->v_full[s]), (uint32_t)(ctl->n_v[s] - 1) & 1u);
             }
         }
-        if (lane == 0 && warp == W_MMA && ctl->last_bar) wait_drain(ctl->last_bar, ctl->last_par);
+        if (lane == 0 && (warp == W_MMA || warp == W_MMA + 1) && ctl->last_bar[warp - W_MMA])
+            wait_drain(ctl->last_bar[warp - W_MMA], ctl->last_par[warp - W_MMA]);
         tc_fence_before();
         __syncthreads();
     }
