@@ -10,21 +10,23 @@
 //
 // A persistent CTA per SM takes pairs of 128-row tiles of one sequence and head, so that each K and V block
 // loaded serves 256 rows.  Warps 0-3 and 4-7 are the softmax of the two tiles, a thread per row (no sum or
-// maximum crosses threads); warp 8 loads by TMA through a ring that runs on across the pairs; warp 9 issues the
-// products.  While one tile's scores are in its softmax, the tensor core works for the other tile: P~
-// overwrites S in TMEM (S is in registers by then), O += P~ V, then S of the next block.
+// maximum crosses threads); warp 8 loads by TMA through a ring that runs on across the pairs; warps 9 and 10 issue
+// the products of a tile each.  S of the next block is formed as soon as this block's is in registers.
 //
-// What bounds it: one exponential a pair.  The special-function unit makes 16 a clock and SM, 128 x 128 pairs
-// take 1024 clocks; S and P V take 128 and at most 256.  So EMULATED of every 32 are computed on the
-// FMA units instead (f2exp2_poly).
+// What bounds it: one exponential a pair.  The special-function unit makes 16 a clock and SM, so 128 x 128 pairs
+// take 1024 clocks; S and P V take 256 each.  Loading S, the maxima, the waits and the rest of a warp's work
+// run beside the other tile's exponentials only in part: a pair of tiles takes about 3500 clocks where the unit alone
+// takes 2048.  Measured and not kept: a quarter or an eighth of the exponentials as polynomials on the FMA units (a
+// block's exponentials are not shortened: the polynomial's instructions take their place), two threads per row
+// (twice the waits), the two tiles' exponentials forced to alternate.
 //
 // P~ enters P V as one bf16 number where O is bf16 (an error of at most 2^-8 a weight, the output's own
-// rounding), and as three (24 bits, every exponential from the special-function unit) where O is fp32.
+// rounding), and as three (24 bits) where O is fp32.
 #include <cuda_bf16.h>
+#include <limits.h>
 #include <math.h>
 #include "../../include/entmax_cache.h"
 #include "common.cuh"
-#include "tau15.cuh"
 #include "internal.h"
 
 namespace entmax {
@@ -40,9 +42,9 @@ constexpr int W_LOAD = 8, W_MMA = 9, PROMPT_THREADS = 384;  // warps 9 and 10: M
 constexpr int REGS_SOFTMAX = 216, REGS_OTHER = 72;
 constexpr int GRID = 148;
 constexpr int LIST = 1024;                   // work items of a CTA and launch
+constexpr int BALANCED = 4;                  // turns of a launch up to which the loads are followed
 constexpr int MAX_SEQS = 4096, MAX_PAIRS = 4096;  // sequences of a call; pairs of a sequence (1 Mi tokens)
 constexpr float RAISE = 8.f;                 // log2 units
-constexpr int EMULATED = 8;                  // of every 32 exponentials
 constexpr float LOG2E_F = 1.4426950408889634f, LN2_F = 0.6931471805599453f;
 
 constexpr int O_Q = 0;                              // Q pairs, two buffers
@@ -70,7 +72,8 @@ struct Ctl {
 constexpr int PROMPT_SMEM = O_CTL + (int)sizeof(Ctl) + 1024;
 static_assert(PROMPT_SMEM <= 227 * 1024, "shared memory");
 // while the work list is made, the ring holds the sequences' pair counts and the counts by size
-static_assert((MAX_SEQS + 3 * (MAX_PAIRS + 2)) * 4 <= NS * 2 * BLOCK16, "list scratch");
+constexpr int LOADS_AT = MAX_SEQS + 2 * (MAX_PAIRS + 2);
+static_assert(LOADS_AT % 4 == 0 && GRID % 4 == 0 && (LOADS_AT + GRID + LIST) * 4 <= NS * 2 * BLOCK16, "list scratch");
 // TMEM columns: S of tile w at 128 w, O at 256 + 64 w, P at 384 + 64 w, so that S of the next block is formed while
 // this block's P is.  Three parts do not fit beside S: the first two then lie over S, and the third at P's place.
 constexpr int TM_S = 0, TM_O = 256, TM_P = 384;
@@ -81,28 +84,6 @@ __device__ __forceinline__ int tile_blocks(const Item& it, int w) {
     return tile * TILE < it.len ? tile + 1 : 0;
 }
 
-// 2^x for two values x <= 127: x = n + f with n the nearest integer (adding and subtracting 1.5 * 2^23), 2^f on
-// [-1/2, 1/2] by a polynomial of degree 4 fitted to the least relative error with 2^0 exact (iteratively
-// reweighted least squares; 2.8e-6), and n added to its exponent.  x is taken as -127 where it is less, and
-// 2^-127 comes out as 0: its exponent field is 0 and the polynomial is 1 there.
-__device__ __forceinline__ uint64_t f2exp2_poly(uint64_t x) {
-    float a, b;
-    f2unpack(x, a, b);
-    x = f2pack(fmaxf(a, -127.f), fmaxf(b, -127.f));
-    const uint64_t magic = f2pack(12582912.f, 12582912.f);
-    const uint64_t t = f2add(x, magic);
-    const uint64_t f = f2sub(x, f2sub(t, magic));
-    uint64_t p = f2pack(9.582852944731712e-3f, 9.582852944731712e-3f);
-    p = f2fma(p, f, f2pack(5.5906426161527634e-2f, 5.5906426161527634e-2f));
-    p = f2fma(p, f, f2pack(2.4024099111557007e-1f, 2.4024099111557007e-1f));
-    p = f2fma(p, f, f2pack(6.931241750717163e-1f, 6.931241750717163e-1f));
-    p = f2fma(p, f, f2pack(1.f, 1.f));
-    float ta, tb;
-    f2unpack(t, ta, tb);
-    f2unpack(p, a, b);
-    return f2pack(__uint_as_float(__float_as_uint(a) + (__float_as_uint(ta) << 23)),
-                  __uint_as_float(__float_as_uint(b) + (__float_as_uint(tb) << 23)));
-}
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -144,7 +125,7 @@ __device__ __forceinline__ void f2split3(uint64_t v, uint32_t& hi, uint32_t& mid
 
 // The CTA's share of the work: all pairs of all sequences and heads, those with the most keys first (by
 // pair number, then sequence, then head: the heads of a group run side by side and share K and V in L2),
-// dealt in turns that change direction.  All threads; scratch: the ring.
+// dealt in turns.  All threads; scratch: the ring.
 __device__ __forceinline__ void make_list(const AttnArgs& a, long long first_item, Item* list, int* scratch, Ctl* ctl) {
     int* pairs = scratch;               // [n] pairs of the sequence, 0 where it is out of range
     int* more = scratch + MAX_SEQS;     // [P + 1] sequences with more than t pairs; first their counts
@@ -190,31 +171,57 @@ __device__ __forceinline__ void make_list(const AttnArgs& a, long long first_ite
     }
     __syncthreads();
     const long long total = ((long long)before[0] + more[0]) * a.H;
-    int n = 0;
-    {
-        const long long left = total - first_item;
-        // turns q with an item for this CTA
-        for (int q = 0; q < LIST; ++q) {
-            const long long at = (long long)q * gridDim.x + ((q & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if (at >= left) {
-                if ((long long)q * gridDim.x >= left) break;
-                continue;  // only in the last turn
-            }
-            n = q + 1;
+    const long long left = total - first_item;
+    const int G = gridDim.x;
+    const int turns = (int)min((long long)LIST, (left + G - 1) / G);
+    // A turn deals the next G items.  Every CTA follows all loads: whoever has least takes the largest item (up to BALANCED
+    // turns; over more, turns that change direction are as even)
+    int* load = scratch + LOADS_AT;      // [GRID], multiples of GRID plus the CTA's number: no two are alike
+    int* my_place = load + GRID;         // [turns] place of this CTA in the turn
+    auto pair_of = [&](int k) {          // the highest t with before[t] + more[t] > k
+        int lo = 0, hi = P;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (before[mid] + more[mid] > k) lo = mid;
+            else hi = mid;
         }
+        return lo;
+    };
+    if (turns <= BALANCED) {
+        for (int k = tid; k < GRID; k += PROMPT_THREADS) load[k] = k < G ? k : INT_MAX;
+        __syncthreads();
+        for (int q = 0; q < turns; ++q) {
+            int place = 0, size = 0;
+            if (tid < G) {
+                const int mine = load[tid];
+                if (q == 0) {
+                    place = tid;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < GRID / 4; ++k) {
+                        const int4 x = reinterpret_cast<const int4*>(load)[k];
+                        place += (x.x < mine) + (x.y < mine) + (x.z < mine) + (x.w < mine);
+                    }
+                }
+                const long long at = first_item + (long long)q * G + place;
+                if (at < total) size = 2 * pair_of((int)(at / a.H)) + 3;  // about half its blocks, and its fixed cost
+                if (tid == blockIdx.x) my_place[q] = place;
+            }
+            __syncthreads();
+            if (tid < G) load[tid] += size * GRID;
+            __syncthreads();
+        }
+    } else {
+        for (int q = tid; q < turns; q += PROMPT_THREADS) my_place[q] = (q & 1) ? G - 1 - blockIdx.x : blockIdx.x;
+        __syncthreads();
     }
+    const int n = turns;
     for (int q = warp; q < n; q += PROMPT_THREADS / 32) {
-        const long long at = first_item + (long long)q * gridDim.x + ((q & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const long long at = first_item + (long long)q * G + my_place[q];
         Item it{0, 0, 0, 0};
         if (at < total) {
             const int k = (int)(at / a.H);
-            // the pair number: the highest t with before[t] + more[t] > k
-            int lo = 0, hi = P;  // before[lo] + more[lo] > k
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (before[mid] + more[mid] > k) lo = mid;
-                else hi = mid;
-            }
+            const int lo = pair_of(k);
             int rank = k - before[lo];  // among the sequences with more than lo pairs
             int s = -1;
             for (int i0 = 0; i0 < a.n_seqs && s < 0; i0 += 32) {
@@ -268,7 +275,27 @@ struct Threshold {
     }
 };
 
-// Softmax: one pass over the blocks.  1.5-entmax: a pass for the largest scores (the exact threshold of the four
+// The exact threshold of the TOP scores scale * top[k] (descending, missing ones -inf), a lower bound of the row's:
+// more scores only raise it.  Sixteen instead of four chunk maxima save one of four passes of sums at 4096 keys.
+constexpr int TOP = 16;
+__device__ __forceinline__ float first_bound(const float (&top)[TOP], float scale) {
+    const float base = scale * top[0];
+    float sum = 0.f, sq = 0.f, bound = -2.f;
+#pragma unroll
+    for (int k = 0; k < TOP; ++k) {
+        const float z = fmaf(scale, top[k], -base);  // <= 0; at or below -2 it is no part of a support
+        if (z > -2.f) {
+            sum += z;
+            sq = fmaf(z, z, sq);
+            const float mean = sum * (1.f / (k + 1)), rest = (4.f - sq) * (1.f / (k + 1)) + mean * mean;
+            const float root = mean - sqrtf(fmaxf(rest, 0.f));
+            if (rest >= 0.f && root <= z) bound = root;
+        }
+    }
+    return base + bound - 1e-5f - 2.4e-7f * fabsf(base);  // less what rounding may have added
+}
+
+// Softmax: one pass over the blocks.  1.5-entmax: a pass for the largest scores (the exact threshold of the
 // largest maxima of 32-key chunks is the first bound), passes that sum over the scores above t until every
 // row of both tiles has settled (three as a rule), and the pass that forms P and P V.  S is formed anew in each: the
 // tensor core does it in a third of the time that the sums take, and no row is ever too dense for a list.
@@ -536,7 +563,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             Threshold th{0.f, 0.f, true};
             bool odd = false;  // 1.5-entmax: infinite or NaN scores
             if (!kSoftmax) {
-                float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
+                float top[TOP];  // the largest chunk maxima, descending
+#pragma unroll
+                for (int k = 0; k < TOP; ++k) top[k] = -INFINITY;
                 for (int j = 0; j < nb; ++j) {
                     float v[4][32];
                     if (!scores(v, j == nb - 1)) break;
@@ -545,16 +574,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     for (int k = 0; k < 4; ++k) {
                         const float cm = max32_nan(v[k]);
                         odd |= cm != cm;
-                        a3 = fmaxf(a3, fminf(a2, cm));
-                        a2 = fmaxf(a2, fminf(a1, cm));
-                        a1 = fmaxf(a1, fminf(a0, cm));
-                        a0 = fmaxf(a0, cm);
+#pragma unroll
+                        for (int t = TOP - 1; t > 0; --t) top[t] = fmaxf(top[t], fminf(top[t - 1], cm));
+                        top[0] = fmaxf(top[0], cm);
                     }
                 }
                 n_kv += nb_all;
-                a0 *= a.scale;
-                th.start(fmaxf(a0 - 2.f, top4_bound<true>(a0, a1 * a.scale, a2 * a.scale, a3 * a.scale, 4.f)));
-                odd |= !(fabsf(a0) < INFINITY);
+                odd |= !(fabsf(top[0] * a.scale) < INFINITY);
+                th.start(first_bound(top, a.scale));
                 if (odd || i >= it.len) {
                     th.start(0.f);
                     th.settled = true;
@@ -644,7 +671,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     const float off = -m * c;
                     off2 = f2pack(off, off);
                 }
-                // P's columns are free once P V of the block before is through (an item's first block: its O was read)
                 if (!kF32 && j > 0) {
                     if (!wait(&ctl->p_empty[w], (uint32_t)(np - 1) & 1u)) break;
                     tc_fence_after();
@@ -660,8 +686,6 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         if (!kSoftmax) {
                             p = f2relu(f2fma(x, h2, t2));
                             p = f2mul(p, p);
-                        } else if (!kF32 && (e / 2) % (32 / EMULATED) == 0) {
-                            p = f2exp2_poly(f2fma(x, c2, off2));
                         } else {
                             float x0, x1;
                             f2unpack(f2fma(x, c2, off2), x0, x1);
@@ -679,12 +703,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                             hi[e >> 1] = pack_bf16(x0, x1);
                         }
                     }
+                    // P's columns are free once P V of the block before is through (an item's first block: its O was read)
                     tmem_st16(p_tm + 16 * k, hi);
                     if (kF32) {
                         tmem_st16(p_tm + 64 + 16 * k, mid);
                         tmem_st16(tmem + lanes + TM_P + 64u * w + 16 * k, lo);
                     }
                 }
+                if (!live) break;
                 tmem_wait_st();
                 if (diag && j == nb_all - 1) {
                     // the rows of V behind the sequence's end belong to others: they must not reach P V, not even

@@ -12,15 +12,10 @@ namespace entmax {
 // Exact threshold (raw units: sum (v - t)^2 = c4 over the kept values) of the set {a0..a3}
 // (a0 >= a1 >= a2 >= a3, missing values -inf), lowered by a rounding margin.  Any subset of a
 // row gives a lower bound of the row's tau: adding scores can only raise the threshold.
-// kShift: computed on the differences from a0, without the cancellation that scores in the hundreds
-// bring (their squares' rounding can pass the margin).  The dense batches' kernels keep the plain form, and
-// with it their results bit for bit.
-template <bool kShift = false>
 __device__ __forceinline__ float top4_bound(float a0, float a1, float a2, float a3, float c4) {
-    const float base = kShift && a0 > -INFINITY ? a0 : 0.f;
-    const float z[4] = {a0 - base, a1 - base, a2 - base, a3 - base};
+    const float z[4] = {a0, a1, a2, a3};
     const float inv[4] = {1.f, 0.5f, 1.f / 3.f, 0.25f};
-    float sum = 0.f, sq = 0.f, bound = z[0] - sqrtf(c4);
+    float sum = 0.f, sq = 0.f, bound = a0 - sqrtf(c4);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         sum += z[k];
@@ -32,7 +27,6 @@ __device__ __forceinline__ float top4_bound(float a0, float a1, float a2, float 
             if (tk <= z[k]) bound = tk;
         }
     }
-    if (kShift) return base + bound - 1e-5f * sqrtf(c4) - 2.4e-7f * fabsf(base);  // two roundings of the sum
     return bound - 1e-5f * sqrtf(c4);
 }
 
