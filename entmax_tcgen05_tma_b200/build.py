@@ -16,7 +16,7 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libentmax_attn.so"
 SOURCES = ["abi.cu", "fwd.cu", "fwd_dense.cu", "fwd_softmax.cu", "bwd.cu", "bwd_saved.cu", "bwd_dense.cu",
            "cache.cu", "cache_attn.cu", "prompt.cu"]
-DEPS = SOURCES + ["common.cuh", "dense.cuh", "tau15.cuh", "ptx.cuh", "internal.h", "cache.cuh"]
+DEPS = SOURCES + ["common.cuh", "dense.cuh", "tau15.cuh", "ptx.cuh", "internal.h", "cache.cuh", "threshold.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

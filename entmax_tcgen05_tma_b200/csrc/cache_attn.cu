@@ -29,6 +29,7 @@
 #include "cache.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "threshold.cuh"
 
 namespace entmax {
 namespace {
@@ -88,11 +89,12 @@ __device__ __forceinline__ int row_len(const TokArgs& a, int i) {
 
 // Exclusive prefix of the rows' page counts into pre[0 .. n] (whole CTA); CTA 0 leaves it in the workspace
 // and reports rows out of range.
+template <int kWarps>
 __device__ __forceinline__ void page_prefix(const TokArgs& a, int* pre) {
-    __shared__ int part[WARPS];
+    __shared__ int part[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int carry = 0;
-    for (int i0 = 0; i0 < a.n; i0 += WARPS * 32) {
+    for (int i0 = 0; i0 < a.n; i0 += kWarps * 32) {
         const int i = i0 + tid;
         const int len = i < a.n ? row_len(a, i) : 0;
         if (len < 0 && blockIdx.x == 0) cache_error(a.c);
@@ -108,7 +110,7 @@ __device__ __forceinline__ void page_prefix(const TokArgs& a, int* pre) {
         __syncthreads();
         int before = carry, all = 0;
 #pragma unroll
-        for (int w = 0; w < WARPS; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             const int p = part[w];
             if (w < warp) before += p;
             all += p;
@@ -198,21 +200,25 @@ __device__ __forceinline__ float load_q(const TokArgs& a, int i, int head0, int 
     return inv;
 }
 
+// Raw scores of a tile of 16 keys from the lane's 16 bytes of keys key_row(g) and 8 + key_row(g).
+__device__ __forceinline__ void tile_scores(const uint4& lo, const uint4& hi, const uint32_t (&qf)[8], float (&c)[4]) {
+    const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+    c[0] = c[1] = c[2] = c[3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)wl[j]), e4m3x2_to_f16x2((uint16_t)wh[j]),
+                                e4m3x2_to_f16x2((uint16_t)(wl[j] >> 16)), e4m3x2_to_f16x2((uint16_t)(wh[j] >> 16))};
+        mma_f16(c, af, qf[2 * j], qf[2 * j + 1]);
+    }
+}
+
 // Raw scores of a page: c[mt][0], c[mt][1]: key row 16 mt + key_row(g), heads 2 t and 2 t + 1; c[mt][2], [3]: 8 rows on.
 __device__ __forceinline__ void page_scores(const uint8_t* sk, const uint32_t (&qf)[8], int g, int t, float (&c)[4][4]) {
     const int r = key_row(g);
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(sk + chunk_at(16 * mt + r, t));
-        const uint4 hi = *reinterpret_cast<const uint4*>(sk + chunk_at(16 * mt + 8 + r, t));
-        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-        c[mt][0] = c[mt][1] = c[mt][2] = c[mt][3] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t af[4] = {e4m3x2_to_f16x2((uint16_t)wl[j]), e4m3x2_to_f16x2((uint16_t)wh[j]),
-                                    e4m3x2_to_f16x2((uint16_t)(wl[j] >> 16)), e4m3x2_to_f16x2((uint16_t)(wh[j] >> 16))};
-            mma_f16(c[mt], af, qf[2 * j], qf[2 * j + 1]);
-        }
+        tile_scores(*reinterpret_cast<const uint4*>(sk + chunk_at(16 * mt + r, t)),
+                    *reinterpret_cast<const uint4*>(sk + chunk_at(16 * mt + 8 + r, t)), qf, c[mt]);
     }
 }
 
@@ -394,7 +400,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) token_softmax_kernel(const TokA
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int* pre = reinterpret_cast<int*>(smem + S_PRE);
-    page_prefix(a, pre);
+    page_prefix<WARPS>(a, pre);
     const Deal deal = deal_of(a, pre[a.n]);
     const int w = warp * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
     if (w >= deal.warps) return;
@@ -558,16 +564,21 @@ __global__ void __launch_bounds__(JT) token_softmax_join_kernel(const TokArgs a)
 // shared memory, one per lane and head.  Lists that fill up are cut again at the threshold of all that
 // they hold.  What is left of a segment, at most GC entries per head, goes to the joining kernel, which
 // takes the best bound of all segments, solves for tau on the entries above it and reads the values of the
-// support.  Rows whose support is too large for a list (flat scores) are flagged; the joining kernel then
-// computes all their scores again from the cache, each time it needs them.
-constexpr int E_STAGES = 4;
-constexpr int LCAP = 20;   // entries per lane and head
-constexpr int E_RING = WARPS * E_STAGES * BLOCK_BYTES;
-constexpr int E_LIST = E_RING;                                  // float2 [2][LCAP][32] per warp
-constexpr int E_LIST_BYTES = 2 * LCAP * 32 * 8;
-constexpr int E_META = E_LIST + WARPS * E_LIST_BYTES;
-constexpr int E_PRE = E_META + WARPS * E_STAGES * 8;
+// support.  Rows with a list that was too small are flagged; the joining kernel lists them again from the
+// cache, and where the support is wider than its own list as well (flat scores) computes the scores anew
+// each time it needs them.
+//
+// A page's keys go straight to registers, the next page's under way meanwhile: the fragments are whole
+// 512-byte runs of the block, there are no values to stage, and the shared memory is free for the lists of sixteen
+// warps.  (Through a ring in shared memory with eight warps this kernel took 57 us where it takes SELF.)
+constexpr int E_WARPS = 16;
+constexpr int LCAP = 28;   // entries per lane and head
+constexpr int E_KEY = 2 * LCAP * 32 * 4;                        // per warp: float [2][LCAP][32], then u16 [2][LCAP][32]
+constexpr int E_LIST_BYTES = E_KEY + 2 * LCAP * 32 * 2;
+constexpr int E_PRE = E_WARPS * E_LIST_BYTES;
+constexpr int E_MAX_LEN = 8192 * PAGE;                          // an entry's key: 13 bits page of the segment, 3 bits place
 constexpr int entmax_smem(int n) { return E_PRE + (n + 1) * 4; }
+static_assert(entmax_smem(MAX_TOKENS) <= 226 * 1024, "shared memory");
 
 // Sum over the eight lanes that hold one head.
 __device__ __forceinline__ float sum_g(float v) {
@@ -577,9 +588,9 @@ __device__ __forceinline__ float sum_g(float v) {
     return v;
 }
 __device__ __forceinline__ float max_g(float v) {
-    v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 4));
-    v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 8));
-    v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, 16));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
     return v;
 }
 // A Newton step on sum max(0, s - t)^2 = 4 given its sums: convex and decreasing, so from a lower bound the
@@ -588,115 +599,128 @@ __device__ __forceinline__ float newton(float t, float s1, float s2) { return s1
 // A bound less what rounding may have added to it.
 __device__ __forceinline__ float safe(float t) { return t - 2e-6f * fmaxf(1.f, fabsf(t)); }
 
-// Raises the cuts of the lane's two heads by `steps` Newton steps on all that the lists hold and drops what
-// lies below.  Warp-collective.
-__device__ __forceinline__ void prune(float2* list, int lane, int steps, float& cut0, float& cut1, int& n0, int& n1) {
-    const int most = __reduce_max_sync(0xffffffffu, max(n0, n1));
-    float t0 = cut0, t1 = cut1;
-    for (int it = 0; it < steps; ++it) {
-        float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
+// The lane's lists of its two heads: entry e of head k at [(k LCAP + e) 32].
+struct Lists {
+    float* s;
+    uint16_t* key;
+    int n0, n1;
+    float cut0, cut1;
+    // Raises the cuts by `steps` Newton steps on all that the eight lanes' lists hold and drops what lies below.
+    __device__ __forceinline__ void prune(int steps) {
+        const int most = __reduce_max_sync(0xffffffffu, max(n0, n1));
+        float t0 = cut0, t1 = cut1;
+        for (int it = 0; it < steps; ++it) {
+            float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
+            for (int e = 0; e < most; ++e) {
+                const float d = e < n0 ? fmaxf(s[e * 32] - t0, 0.f) : 0.f;
+                const float f = e < n1 ? fmaxf(s[(LCAP + e) * 32] - t1, 0.f) : 0.f;
+                a1 += d;
+                a2 = fmaf(d, d, a2);
+                b1 += f;
+                b2 = fmaf(f, f, b2);
+            }
+            t0 = newton(t0, sum_g(a1), sum_g(a2));
+            t1 = newton(t1, sum_g(b1), sum_g(b2));
+        }
+        cut0 = fmaxf(cut0, safe(t0));
+        cut1 = fmaxf(cut1, safe(t1));
+        int k0 = 0, k1 = 0;
         for (int e = 0; e < most; ++e) {
-            const float d = e < n0 ? fmaxf(list[e * 32 + lane].x - t0, 0.f) : 0.f;
-            const float f = e < n1 ? fmaxf(list[(LCAP + e) * 32 + lane].x - t1, 0.f) : 0.f;
-            a1 += d;
-            a2 = fmaf(d, d, a2);
-            b1 += f;
-            b2 = fmaf(f, f, b2);
+            if (e < n0) {
+                const float x = s[e * 32];
+                const uint16_t y = key[e * 32];
+                if (x > cut0) {
+                    s[k0 * 32] = x;
+                    key[k0++ * 32] = y;
+                }
+            }
+            if (e < n1) {
+                const float x = s[(LCAP + e) * 32];
+                const uint16_t y = key[(LCAP + e) * 32];
+                if (x > cut1) {
+                    s[(LCAP + k1) * 32] = x;
+                    key[(LCAP + k1++) * 32] = y;
+                }
+            }
         }
-        t0 = newton(t0, sum_g(a1), sum_g(a2));
-        t1 = newton(t1, sum_g(b1), sum_g(b2));
+        n0 = k0;
+        n1 = k1;
     }
-    cut0 = fmaxf(cut0, safe(t0));
-    cut1 = fmaxf(cut1, safe(t1));
-    int k0 = 0, k1 = 0;
-    for (int e = 0; e < most; ++e) {
-        if (e < n0) {
-            const float2 x = list[e * 32 + lane];
-            if (x.x > cut0) list[k0++ * 32 + lane] = x;
-        }
-        if (e < n1) {
-            const float2 x = list[(LCAP + e) * 32 + lane];
-            if (x.x > cut1) list[(LCAP + k1++) * 32 + lane] = x;
-        }
-    }
-    n0 = k0;
-    n1 = k1;
-}
+};
 
-__global__ void __launch_bounds__(WARPS * 32, 1) token_entmax_kernel(const TokArgs a) {
+__global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const TokArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int* pre = reinterpret_cast<int*>(smem + E_PRE);
-    page_prefix(a, pre);
+    page_prefix<E_WARPS>(a, pre);
     const Deal deal = deal_of(a, pre[a.n]);
     const int w = warp * gridDim.x + blockIdx.x;
     if (w >= deal.warps) return;
-    uint8_t* ring = smem + warp * E_STAGES * BLOCK_BYTES;
-    float2* list = reinterpret_cast<float2*>(smem + E_LIST + warp * E_LIST_BYTES);
-    float2* metas = reinterpret_cast<float2*>(smem + E_META) + warp * E_STAGES;  // scale, keys
-    const uint32_t ring_u = smem_u32(ring);
+    Lists li;
+    li.s = reinterpret_cast<float*>(smem + warp * E_LIST_BYTES) + lane;
+    li.key = reinterpret_cast<uint16_t*>(smem + warp * E_LIST_BYTES + E_KEY) + lane;
     const int r = key_row(g);
 
     const long long u0 = deal.start(w), u1 = deal.start(w + 1);
     for (long long u = u0; u < u1;) {
         const Segment s = segment_at(a, pre, u, u1);
+        PageRun<false> run;
+        run.load(a, s, s.page0);
+        struct Page {
+            uint4 k[8];  // the lane's 16 bytes of its two keys of each tile
+            float ks;
+            int valid;
+        };
+        auto fetch = [&](int p, Page& b) {
+            b.valid = 0;
+            if (p >= s.page1) return;
+            if (p >= run.base + 32) run.load(a, s, p);
+            const int phys = __shfl_sync(0xffffffffu, run.phys, p - run.base);
+            b.ks = __shfl_sync(0xffffffffu, run.ks, p - run.base);
+            if (phys < 0) return;
+            b.valid = min(PAGE, s.len - p * PAGE);
+            const uint4* src = reinterpret_cast<const uint4*>(a.c.K + a.c.block(a.layer, phys, s.kvh) * BLOCK_BYTES) + r * 4 + t;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b.k[k] = __ldg(src + 32 * k);
+        };
+        Page pa, pb;
+        fetch(s.page0, pa);
         uint32_t qf[8];
         const float qinv = load_q(a, s.i, s.head0, s.heads, qf);
         const float f0 = a.scale * __shfl_sync(0xffffffffu, qinv, 8 * t);
         const float f1 = a.scale * __shfl_sync(0xffffffffu, qinv, 8 * t + 4);
-        PageRun<false> run;
-        run.load(a, s, s.page0);
-        auto fetch = [&](int p) {
-            if (p < s.page1) {
-                if (p >= run.base + 32) run.load(a, s, p);
-                const int phys = __shfl_sync(0xffffffffu, run.phys, p - run.base);
-                const float ks = __shfl_sync(0xffffffffu, run.ks, p - run.base);
-                const int st = (p - s.page0) % E_STAGES;
-                if (lane == 0) metas[st] = make_float2(ks, __int_as_float(phys < 0 ? 0 : min(PAGE, s.len - p * PAGE)));
-                if (phys >= 0) load_block(ring_u + st * BLOCK_BYTES, a.c.K + a.c.block(a.layer, phys, s.kvh) * BLOCK_BYTES, lane);
-            }
-            cp_commit();
-        };
         // a head that the group does not have takes nothing
         const bool use0 = 2 * t < s.heads, use1 = 2 * t + 1 < s.heads;
-        float cut0 = use0 ? -INFINITY : INFINITY, cut1 = use1 ? -INFINITY : INFINITY;
-        int n0 = 0, n1 = 0;
+        li.cut0 = use0 ? -INFINITY : INFINITY;
+        li.cut1 = use1 ? -INFINITY : INFINITY;
+        li.n0 = li.n1 = 0;
         bool odd0 = false, odd1 = false, over0 = false, over1 = false;  // not finite; lists too small
-#pragma unroll
-        for (int k = 0; k < E_STAGES - 1; ++k) fetch(s.page0 + k);
-        for (int p = s.page0; p < s.page1; ++p) {
-            fetch(p + E_STAGES - 1);
-            cp_wait<E_STAGES - 1>();
-            __syncwarp();
-            const int st = (p - s.page0) % E_STAGES;
-            float c[4][4];
-            const float2 meta = metas[st];
-            page_scores(ring + st * BLOCK_BYTES, qf, g, t, c);
-            __syncwarp();
-            const int valid = __float_as_int(meta.y);
-            float x0 = -INFINITY, x1 = -INFINITY;
+        bool fresh = true;
+        auto process = [&](int p, const Page& b) {
+            float c[4][4], x0 = -INFINITY, x1 = -INFINITY;
+            const float h0 = f0 * b.ks, h1 = f1 * b.ks;
 #pragma unroll
             for (int mt = 0; mt < 4; ++mt) {
-                c[mt][0] *= f0 * meta.x;
-                c[mt][1] *= f1 * meta.x;
-                c[mt][2] *= f0 * meta.x;
-                c[mt][3] *= f1 * meta.x;
-                if (valid < PAGE) {
-                    if (16 * mt + r >= valid) c[mt][0] = c[mt][1] = -INFINITY;
-                    if (16 * mt + 8 + r >= valid) c[mt][2] = c[mt][3] = -INFINITY;
+                tile_scores(b.k[2 * mt], b.k[2 * mt + 1], qf, c[mt]);
+                c[mt][0] *= h0;
+                c[mt][1] *= h1;
+                c[mt][2] *= h0;
+                c[mt][3] *= h1;
+                if (b.valid < PAGE) {
+                    if (16 * mt + r >= b.valid) c[mt][0] = c[mt][1] = -INFINITY;
+                    if (16 * mt + 8 + r >= b.valid) c[mt][2] = c[mt][3] = -INFINITY;
                 }
                 x0 = max_nan(x0, max_nan(c[mt][0], c[mt][2]));
                 x1 = max_nan(x1, max_nan(c[mt][1], c[mt][3]));
             }
             // anything above the cuts? (a NaN compares as yes)
-            if (!__any_sync(0xffffffffu, !(x0 <= cut0) || !(x1 <= cut1))) continue;
-            x0 = max_g(x0);
-            x1 = max_g(x1);
-            odd0 |= valid > 0 && !(fabsf(x0) < INFINITY);
-            odd1 |= valid > 0 && !(fabsf(x1) < INFINITY);
-            if (p == s.page0 && valid > 0) {
+            if (!__any_sync(0xffffffffu, !(x0 <= li.cut0) || !(x1 <= li.cut1))) return;
+            odd0 |= !(x0 < INFINITY);
+            odd1 |= !(x1 < INFINITY);
+            if (fresh && b.valid > 0) {
                 // the first page's own threshold, from its largest score less two
-                float t0 = x0 - 2.f, t1 = x1 - 2.f;
+                fresh = false;
+                float t0 = max_g(x0) - 2.f, t1 = max_g(x1) - 2.f;
                 for (int it = 0; it < 4; ++it) {
                     float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
 #pragma unroll
@@ -712,34 +736,50 @@ __global__ void __launch_bounds__(WARPS * 32, 1) token_entmax_kernel(const TokAr
                     t0 = newton(t0, sum_g(a1), sum_g(a2));
                     t1 = newton(t1, sum_g(b1), sum_g(b2));
                 }
-                cut0 = fmaxf(cut0, safe(t0));
-                cut1 = fmaxf(cut1, safe(t1));
+                li.cut0 = fmaxf(li.cut0, safe(t0));
+                li.cut1 = fmaxf(li.cut1, safe(t1));
             }
-            cut0 = fmaxf(cut0, safe(x0 - 2.f));
-            cut1 = fmaxf(cut1, safe(x1 - 2.f));
-            const int key0 = p * PAGE + r;
+            const int code0 = (p - s.page0) << 3;
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < 4; ++mt) {
+                const bool hit = c[mt][0] > li.cut0 || c[mt][2] > li.cut0 || c[mt][1] > li.cut1 || c[mt][3] > li.cut1;
+                if (!__any_sync(0xffffffffu, hit)) continue;
 #pragma unroll
                 for (int q = 0; q < 4; q += 2) {
-                    const int key = key0 + 16 * mt + 4 * q;
-                    if (c[mt][q] > cut0) list[n0++ * 32 + lane] = make_float2(c[mt][q], __int_as_float(key));
-                    if (c[mt][q + 1] > cut1) list[(LCAP + n1++) * 32 + lane] = make_float2(c[mt][q + 1], __int_as_float(key));
+                    const uint16_t code = (uint16_t)(code0 + 2 * mt + (q >> 1));
+                    if (c[mt][q] > li.cut0) {
+                        li.s[li.n0 * 32] = c[mt][q];
+                        li.key[li.n0++ * 32] = code;
+                    }
+                    if (c[mt][q + 1] > li.cut1) {
+                        li.s[(LCAP + li.n1) * 32] = c[mt][q + 1];
+                        li.key[(LCAP + li.n1++) * 32] = code;
+                    }
                 }
-            if (__any_sync(0xffffffffu, max(n0, n1) > LCAP - 8)) {
-                prune(list, lane, 4, cut0, cut1, n0, n1);
-                // still no room for the next page: give the head up
-                over0 |= __any_sync(0xffffffffu, n0 > LCAP - 8) && sum_g(n0 > LCAP - 8 ? 1.f : 0.f) > 0.f;
-                over1 |= __any_sync(0xffffffffu, n1 > LCAP - 8) && sum_g(n1 > LCAP - 8 ? 1.f : 0.f) > 0.f;
-                if (over0) n0 = 0;
-                if (over1) n1 = 0;
             }
+            if (__any_sync(0xffffffffu, max(li.n0, li.n1) > LCAP - 8)) {
+                li.prune(4);
+                // still no room for the next page: give the head up
+                over0 |= sum_g(li.n0 > LCAP - 8 ? 1.f : 0.f) > 0.f;
+                over1 |= sum_g(li.n1 > LCAP - 8 ? 1.f : 0.f) > 0.f;
+                if (over0) li.n0 = 0;
+                if (over1) li.n1 = 0;
+            }
+        };
+        for (int p = s.page0; p < s.page1; p += 2) {
+            fetch(p + 1, pb);
+            process(p, pa);
+            if (p + 1 >= s.page1) break;
+            fetch(p + 2, pa);
+            process(p + 1, pb);
         }
-        prune(list, lane, 6, cut0, cut1, n0, n1);
+        li.prune(6);
+        odd0 = sum_g(odd0 ? 1.f : 0.f) > 0.f;
+        odd1 = sum_g(odd1 ? 1.f : 0.f) > 0.f;
         // the heads' entries, lanes in order
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int n = k ? n1 : n0;
+            const int n = k ? li.n1 : li.n0;
             int x = n;
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
@@ -753,17 +793,23 @@ __global__ void __launch_bounds__(WARPS * 32, 1) token_entmax_kernel(const TokAr
             const size_t slot = (size_t)(w + s.row) * a.heads + h;
             if (g == 0) {
                 a.cand_n[slot] = odd ? -2 : over ? -1 : total;
-                a.cand_cut[slot] = k ? cut1 : cut0;
+                a.cand_cut[slot] = k ? li.cut1 : li.cut0;
             }
             if (!odd && !over)
-                for (int e = 0; e < n; ++e) a.cand[slot * GC + x - n + e] = list[(k * LCAP + e) * 32 + lane];
+                for (int e = 0; e < n; ++e) {
+                    const int code = li.key[(k * LCAP + e) * 32];
+                    const int key = (s.page0 + (code >> 3)) * PAGE + ((code >> 1) & 3) * 16 + (code & 1) * 8 + r;
+                    a.cand[slot * GC + x - n + e] = make_float2(li.s[(k * LCAP + e) * 32], __int_as_float(key));
+                }
         }
-        __syncwarp();  // the lists and stages are the next segment's
+        __syncwarp();  // the lists are the next segment's
         u += s.page1 - s.page0;
     }
 }
 
-constexpr int JCAP = 2048;  // entries above the joint bound that the joining kernel holds, a quarter per warp
+constexpr int EJ_WARPS = 8, EJT = EJ_WARPS * 32;  // the joining kernel, one CTA per (token, query head)
+constexpr int JCAP = 2048;                        // entries above the joint bound that it holds, an eighth per warp
+constexpr int JW = JCAP / EJ_WARPS;
 
 __device__ __forceinline__ float4 block_sum4(float4 v, float4* part) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -777,27 +823,33 @@ __device__ __forceinline__ float4 block_sum4(float4 v, float4* part) {
     __syncthreads();
     if (lane == 0) part[warp] = v;
     __syncthreads();
-    const float4 a = part[0], b = part[1], c = part[2], d = part[3];
-    return make_float4((a.x + b.x) + (c.x + d.x), (a.y + b.y) + (c.y + d.y), (a.z + b.z) + (c.z + d.z), (a.w + b.w) + (c.w + d.w));
+    float4 s = part[0];
+#pragma unroll
+    for (int k = 1; k < EJ_WARPS; ++k) {
+        s.x += part[k].x;
+        s.y += part[k].y;
+        s.z += part[k].z;
+        s.w += part[k].w;
+    }
+    return s;
 }
 
 __device__ __forceinline__ float4 e4m3x4_to_f32(uint32_t v) {
     const uint32_t lo = e4m3x2_to_f16x2((uint16_t)v), hi = e4m3x2_to_f16x2((uint16_t)(v >> 16));
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    const float2 a = unpack_f16(lo), b = unpack_f16(hi);
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-// One CTA per (token, query head).
-__global__ void __launch_bounds__(JT) token_entmax_join_kernel(const TokArgs a) {
+__global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a) {
     __shared__ float2 ent[JCAP];
-    __shared__ float4 part[4];
+    __shared__ float4 part[EJ_WARPS];
     __shared__ float qs[64];
-    __shared__ float red[4];
-    __shared__ int counts[4];
-    __shared__ float4 osum[8][16];
-    __shared__ short seg_n[GRID * WARPS];
-    __shared__ float wts[JT];
-    __shared__ const uint8_t* vat[JT];
+    __shared__ float red[EJ_WARPS];
+    __shared__ int counts[EJ_WARPS];
+    __shared__ float4 osum[EJT / 16][16];
+    __shared__ short seg_n[GRID * E_WARPS];
+    __shared__ float wts[EJT];
+    __shared__ const uint8_t* vat[EJT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x / a.H, head = blockIdx.x - i * a.H;
     const int first = a.prefix[i], pages = a.prefix[i + 1] - first;
@@ -819,13 +871,12 @@ __global__ void __launch_bounds__(JT) token_entmax_join_kernel(const TokArgs a) 
     const int segs = r.w1 - r.w0 + 1;
     const int seq = a.seqs[i], len = a.c.lens[seq];
     const int* table = a.c.table + (size_t)seq * a.c.max_pages;
-    if (tid < 64) qs[tid] = __bfloat162float(a.Q[(long long)i * a.q_stride + head * 64 + tid]) * a.scale;
 
     // the best bound of all segments, and whether the lists are whole
     const size_t slot0 = ((size_t)r.w0 + ((size_t)i * a.c.Hkv + kvh) * a.groups + grp) * a.heads + h;  // then one slot per warp
     float cut = -INFINITY;
     int least = 0;
-    for (int k = tid; k < segs; k += JT) {
+    for (int k = tid; k < segs; k += EJT) {
         const int m = a.cand_n[slot0 + (size_t)k * a.heads];
         seg_n[k] = (short)m;
         least = min(least, m);
@@ -839,60 +890,29 @@ __global__ void __launch_bounds__(JT) token_entmax_join_kernel(const TokArgs a) 
         counts[warp] = least;
     }
     __syncthreads();
-    cut = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    least = min(min(counts[0], counts[1]), min(counts[2], counts[3]));
+#pragma unroll
+    for (int k = 0; k < EJ_WARPS; ++k) {
+        cut = fmaxf(cut, red[k]);
+        least = min(least, counts[k]);
+    }
     __syncthreads();
     if (least == -2) {
         put(NAN, NAN);
         return;
     }
-    if (cut == -INFINITY && least == 0) {  // every page out of range
+    if (cut == -INFINITY) {  // every page out of range
         put(0.f, INFINITY);
         return;
     }
-    // entries above the bound: each warp takes every fourth segment, in order, into its quarter of the list
-    bool listed = least == 0;
-    if (listed) {
-        float2* mine = ent + warp * (JCAP / 4);
-        int at = 0;
-        for (int k0 = warp; k0 < segs; k0 += 16) {
-            float2 x[4];
-            int n[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {  // four segments' first entries in flight
-                const int k = k0 + 4 * q;
-                n[q] = k < segs ? seg_n[k] : 0;
-                x[q] = make_float2(-INFINITY, 0.f);
-                if (lane < n[q]) x[q] = a.cand[(slot0 + (size_t)k * a.heads) * GC + lane];
-            }
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int k = k0 + 4 * q;
-                for (int e = lane;;) {
-                    const uint32_t keep = __ballot_sync(0xffffffffu, x[q].x > cut);
-                    const int to = at + __popc(keep & ((1u << lane) - 1u));
-                    if (x[q].x > cut && to < JCAP / 4) mine[to] = x[q];
-                    at += __popc(keep);
-                    e += 32;
-                    if (e - lane >= n[q]) break;
-                    x[q] = make_float2(-INFINITY, 0.f);
-                    if (e < n[q]) x[q] = a.cand[(slot0 + (size_t)k * a.heads) * GC + e];
-                }
-            }
-        }
-        if (lane == 0) counts[warp] = at;
-    }
-    __syncthreads();
-    int total = 0;
-    if (listed) {
-        listed = max(max(counts[0], counts[1]), max(counts[2], counts[3])) <= JCAP / 4;
-        total = counts[0] + counts[1] + counts[2] + counts[3];
-    }
-    const int b1 = counts[0], b2 = b1 + counts[1], b3 = b2 + counts[2];
-    auto place = [&](int j) {  // entry j of the four quarters behind each other
-        return j < b1 ? j : j < b2 ? JCAP / 4 + j - b1 : j < b3 ? JCAP / 2 + j - b2 : 3 * (JCAP / 4) + j - b3;
+    // entries above the bound, each warp's in its share of the list
+    float2* mine = ent + warp * JW;
+    int at = 0;
+    auto append = [&](float2 x) {
+        const uint32_t keep = __ballot_sync(0xffffffffu, x.x > cut);
+        const int to = at + __popc(keep & ((1u << lane) - 1u));
+        if (x.x > cut && to < JW) mine[to] = x;
+        at += __popc(keep);
     };
-
     // the score of key j again from the cache; -inf for a page out of range
     auto score = [&](int j) -> float {
         const int phys = table[j / PAGE];
@@ -913,42 +933,69 @@ __global__ void __launch_bounds__(JT) token_entmax_join_kernel(const TokArgs a) 
         }
         return acc * a.c.ks[blk];
     };
-    const int count = listed ? total : len;
-    // Newton's method from the bound until it stops rising, then the closed form on the support it leaves:
-    // tau = mean - sqrt(4 / k - variance) of the k scores above
-    float t = cut;
-    if (!listed) {
-        // bounds of flagged segments may be far below: start at the row's largest score less two
-        float m = -INFINITY;
-        for (int j = tid; j < len; j += JT) m = max_nan(m, score(j));
+    if (least == 0) {
+        // sixteen segments a step and warp, eight lanes a segment
+        const int sub = lane >> 3, le = lane & 7;
+        for (int k0 = warp * 16; k0 < segs; k0 += EJ_WARPS * 16) {
+            float2 x[4];
+            int n[4];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (lane == 0) red[warp] = m;
+            for (int q = 0; q < 4; ++q) {
+                const int k = k0 + 4 * q + sub;
+                n[q] = k < segs ? seg_n[k] : 0;
+                x[q] = make_float2(-INFINITY, 0.f);
+                if (le < n[q]) x[q] = a.cand[(slot0 + (size_t)k * a.heads) * GC + le];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                append(x[q]);
+                const int most = __reduce_max_sync(0xffffffffu, n[q]);
+                for (int e = 8 + le; e - le < most; e += 8) {
+                    float2 y = make_float2(-INFINITY, 0.f);
+                    if (e < n[q]) y = a.cand[(slot0 + (size_t)(k0 + 4 * q + sub) * a.heads) * GC + e];
+                    append(y);
+                }
+            }
+        }
+    } else {
+        if (tid < 64) qs[tid] = __bfloat162float(a.Q[(long long)i * a.q_stride + head * 64 + tid]) * a.scale;
         __syncthreads();
-        m = max_nan(max_nan(red[0], red[1]), max_nan(red[2], red[3]));
-        if (!(fabsf(m) < INFINITY)) {
-            put(NAN, NAN);
-            return;
-        }
-        t = fmaxf(t, safe(m - 2.f));
+        const int j0 = (int)((long long)len * warp / EJ_WARPS), j1 = (int)((long long)len * (warp + 1) / EJ_WARPS);
+        for (int j = j0 + lane; j - lane < j1; j += 32)
+            append(make_float2(j < j1 ? score(j) : -INFINITY, __int_as_float(j)));
     }
-    for (int it = 0; it < 24; ++it) {
-        float s1 = 0.f, s2 = 0.f;
-        for (int j = tid; j < count; j += JT) {
-            const float x = fmaxf((listed ? ent[place(j)].x : score(j)) - t, 0.f);
-            s1 += x;
-            s2 = fmaf(x, x, s2);
-        }
-        const float4 s = block_sum4(make_float4(s1, s2, 0.f, 0.f), part);
-        const float next = newton(t, s.x, s.y);
-        const bool done = next - t <= 1e-6f * fmaxf(1.f, fabsf(t));  // uniform
-        t = next;
-        if (done) break;
+    if (lane == 0) counts[warp] = at;
+    __syncthreads();
+    int total = 0, most = 0, begin[EJ_WARPS];
+#pragma unroll
+    for (int k = 0; k < EJ_WARPS; ++k) {
+        begin[k] = total;
+        total += counts[k];
+        most = max(most, counts[k]);
     }
-    {
-        float k = 0.f, s1 = 0.f, s2 = 0.f;  // of x = s - t over the support
-        for (int j = tid; j < count; j += JT) {
-            const float x = (listed ? ent[place(j)].x : score(j)) - t;
+    bool listed = most <= JW;
+    if (!listed && least == 0) {  // too many entries of whole lists: as a flat row
+        if (tid < 64) qs[tid] = __bfloat162float(a.Q[(long long)i * a.q_stride + head * 64 + tid]) * a.scale;
+        __syncthreads();
+    }
+    auto place = [&](int j) {  // entry j of the warps' shares behind each other
+        int w = 0, b = 0;
+#pragma unroll
+        for (int k = 1; k < EJ_WARPS; ++k)
+            if (j >= begin[k]) {
+                w = k;
+                b = begin[k];
+            }
+        return w * JW + j - b;
+    };
+    const int count = listed ? total : len;
+    Threshold th;
+    th.start(cut);
+    bool before = false;  // one pass beyond the settled one: it costs little here, and leaves nothing of the error
+    for (int pass = 1; pass <= MOST_PASSES; ++pass) {
+        float k = 0.f, s1 = 0.f, s2 = 0.f;
+        for (int j = tid; j < count; j += EJT) {
+            const float x = (listed ? ent[place(j)].x : score(j)) - th.t;
             if (x > 0.f) {
                 k += 1.f;
                 s1 += x;
@@ -956,30 +1003,29 @@ __global__ void __launch_bounds__(JT) token_entmax_join_kernel(const TokArgs a) 
             }
         }
         const float4 s = block_sum4(make_float4(k, s1, s2, 0.f), part);
-        if (s.x > 0.f) {
-            const float mean = s.y / s.x, var = fmaxf(s.z / s.x - mean * mean, 0.f);
-            const float fix = mean - sqrtf(fmaxf(4.f / s.x - var, 0.f));
-            if (fabsf(fix) <= 1e-5f * fmaxf(1.f, fabsf(t))) t += fix;
-        }
+        th.step(s.x, s.y, s.z, pass);  // the same in all threads
+        if (th.settled && before) break;
+        before = th.settled;
     }
-    // O = sum p_j V_j.  Weights and places of up to JT keys at a time in shared memory, then eight groups of 16
-    // lanes, a key each, four dimensions a lane
+    const float t = th.t;
+    // O = sum p_j V_j.  Weights and places of up to EJT keys at a time in shared memory, then groups of 16 lanes, a
+    // key each, four dimensions a lane
     const int grp16 = tid >> 4, l16 = tid & 15;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < count; j0 += JT) {
+    for (int j0 = 0; j0 < count; j0 += EJT) {
         const int j = j0 + tid;
         float w = 0.f;
-        const uint8_t* at = a.c.V;
+        const uint8_t* va = a.c.V;
         if (j < count) {
             float2 x = make_float2(0.f, __int_as_float(j));
             if (listed) x = ent[place(j)];
             else x.x = score(j);
-            const float d = x.x - t;
-            if (d > 0.f) {
+            const float e = x.x - t;
+            if (e > 0.f) {
                 const int key = __float_as_int(x.y);
                 const size_t blk = a.c.block(a.layer, table[key / PAGE], kvh);
-                w = 0.25f * d * d * a.c.vs[blk];
-                at += blk * BLOCK_BYTES + (key % PAGE) * 64;
+                w = 0.25f * e * e * a.c.vs[blk];
+                va += blk * BLOCK_BYTES + (key % PAGE) * 64;
             }
         }
         // the keys of the support to the front, in order
@@ -987,16 +1033,19 @@ __global__ void __launch_bounds__(JT) token_entmax_join_kernel(const TokArgs a) 
         __syncthreads();  // the batch before is read
         if (lane == 0) counts[warp] = __popc(keep);
         __syncthreads();
-        int to = __popc(keep & ((1u << lane) - 1u));
-        for (int v = 0; v < warp; ++v) to += counts[v];
+        int to = __popc(keep & ((1u << lane) - 1u)), m = 0;
+#pragma unroll
+        for (int v = 0; v < EJ_WARPS; ++v) {
+            if (v < warp) to += counts[v];
+            m += counts[v];
+        }
         if (w != 0.f) {
             wts[to] = w;
-            vat[to] = at;
+            vat[to] = va;
         }
-        const int m = counts[0] + counts[1] + counts[2] + counts[3];
         __syncthreads();
 #pragma unroll 4
-        for (int e = grp16; e < m; e += 8) {
+        for (int e = grp16; e < m; e += EJT / 16) {
             const float p = wts[e];
             const float4 v = e4m3x4_to_f32(__ldg(reinterpret_cast<const uint32_t*>(vat[e]) + l16));
             o.x = fmaf(p, v.x, o.x);
@@ -1010,7 +1059,7 @@ __global__ void __launch_bounds__(JT) token_entmax_join_kernel(const TokArgs a) 
     if (tid < 16) {
         o = osum[0][tid];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) {
+        for (int k = 1; k < EJT / 16; ++k) {
             o.x += osum[k][tid].x;
             o.y += osum[k][tid].y;
             o.z += osum[k][tid].z;
@@ -1033,7 +1082,7 @@ bool is_softmax(float alpha) { return fabsf(alpha - 1.f) < 1e-4f; }
 
 size_t entmax_slots(int n, int H, int Hkv) {
     const int G = H / Hkv, groups = (G + HG - 1) / HG;
-    return ((size_t)GRID * WARPS + (size_t)n * Hkv * groups) * std::min(G, HG);
+    return ((size_t)GRID * E_WARPS + (size_t)n * Hkv * groups) * std::min(G, HG);
 }
 size_t ws_bytes_of(int n, int H, int Hkv, float alpha) {
     const bool soft = is_softmax(alpha);
@@ -1065,7 +1114,7 @@ int entmax_cache_attn(const entmax_cache* c, int layer, const void* Q, long long
     if (out_dtype != ENTMAX_BF16 && out_dtype != ENTMAX_F32) return ENTMAX_ERR_ARG;
     if (layer < 0 || layer >= c->n_layers) return ENTMAX_ERR_ARG;
     if (c->H_kv < 1 || H % c->H_kv != 0) return ENTMAX_ERR_ARG;
-    if (n > MAX_TOKENS) return ENTMAX_ERR_UNSUPPORTED;
+    if (n > MAX_TOKENS || (!is_softmax(alpha) && max_len > E_MAX_LEN)) return ENTMAX_ERR_UNSUPPORTED;
     if (n == 0 || H == 0) return ENTMAX_OK;
     if (max_len > (long long)c->max_pages * PAGE) return ENTMAX_ERR_ARG;
     if (!Q || !seqs || !O || !tau || !aligned(Q, 16) || !aligned(seqs, 4) || !aligned(O, 16) || !aligned(tau, 4))
@@ -1091,7 +1140,7 @@ int entmax_cache_attn(const entmax_cache* c, int layer, const void* Q, long long
     a.O = O;
     a.out_f32 = out_dtype == ENTMAX_F32;
     a.tau = tau;
-    a.warps = GRID * WARPS;
+    a.warps = GRID * (soft ? WARPS : E_WARPS);
     a.heads = std::min(a.G, HG);
     const size_t slots = soft ? (size_t)a.warps * 2 * HG : entmax_slots(n, H, c->H_kv);
     uint8_t* p = static_cast<uint8_t*>(workspace);
@@ -1112,11 +1161,11 @@ int entmax_cache_attn(const entmax_cache* c, int layer, const void* Q, long long
     rc = abi_record(ensure_smem_attr(f, soft ? softmax_smem(MAX_TOKENS) : entmax_smem(MAX_TOKENS), soft ? 17 : 18));
     if (rc) return rc;
     if (soft) token_softmax_kernel<<<GRID, WARPS * 32, softmax_smem(n), stream>>>(a);
-    else token_entmax_kernel<<<GRID, WARPS * 32, entmax_smem(n), stream>>>(a);
+    else token_entmax_kernel<<<GRID, E_WARPS * 32, entmax_smem(n), stream>>>(a);
     rc = abi_record(cudaGetLastError());
     if (rc) return rc;
     if (soft) token_softmax_join_kernel<<<n * H, JT, 0, stream>>>(a);
-    else token_entmax_join_kernel<<<n * H, JT, 0, stream>>>(a);
+    else token_entmax_join_kernel<<<n * H, EJT, 0, stream>>>(a);
     return abi_record(cudaGetLastError());
 }
 

@@ -108,7 +108,8 @@ ENTMAX_API int entmax_cache_append(const entmax_cache* c, int layer, const void*
  *   Q           bf16, token i's query head h at [i * q_stride + 64 h]; q_stride in elements, a multiple of 8, at
  *               least 64 H; 16-byte aligned.
  *   seqs        device int32 [n], row i's sequence; a sequence may be named several times.
- *   max_len     no sequence of the list is longer (at most 64 max_pages).
+ *   max_len     no sequence of the list is longer: at most 64 max_pages, and for alpha 1.5 at most 524288 (else
+ *               ENTMAX_ERR_UNSUPPORTED).
  *   alpha       1.5 (1.5-entmax) or within 1e-4 of 1 (softmax); other values in (1, 2] return
  *               ENTMAX_ERR_UNSUPPORTED, any others ENTMAX_ERR_ARG.
  *   H           query heads, a multiple of H_kv.
