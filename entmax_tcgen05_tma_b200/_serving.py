@@ -5,7 +5,6 @@ stream is given, on that device's current torch stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import torch
@@ -22,21 +21,37 @@ class _CacheStruct(ctypes.Structure):
                 ("H_kv", ctypes.c_int), ("n_seqs", ctypes.c_int), ("max_pages", ctypes.c_int)]
 
 
+class _Here:
+    """A context that does nothing (the tensors' device is current already)."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
+
+
 def _on(device):
     """The device made current for the call, where it is not already."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _handle(stream, device) -> int:
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError("the stream is on %s, the tensors on %s" % (s.device, device))
-    return int(s.cuda_stream)
+    if stream is None:
+        return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+    return int(stream.cuda_stream)
 
 
 def _need(name, t, shape, dtype, device):
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous() \
+            and device is not None:
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != dtype:
@@ -49,13 +64,13 @@ def _need(name, t, shape, dtype, device):
         raise ValueError("%s must be contiguous" % name)
 
 
-def _rows(name, t, heads, device, dtypes=(torch.bfloat16,)):
+def _rows(name, t, heads, device):
     """Checks a [T, heads, 64] tensor whose tokens may lie apart (a slice of a fused projection) and
     returns its token stride in elements."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.dtype is not torch.bfloat16:
+        raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
     if t.dim() != 3 or t.shape[2] != 64 or (heads is not None and t.shape[1] != heads):
         raise ValueError("%s has shape %s, expected [T, %s, 64]" % (name, tuple(t.shape), "heads" if heads is None else heads))
     if device is not None and t.device != device:
@@ -64,6 +79,8 @@ def _rows(name, t, heads, device, dtypes=(torch.bfloat16,)):
     least = 64 * h
     if T == 0 or h == 0:
         return max(least, 64)
+    if t.is_contiguous():
+        return least
     s0, s1, s2 = t.stride()
     if s2 != 1 or (h > 1 and s1 != 64):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
@@ -88,13 +105,15 @@ class EntmaxCache:
     """
 
     __slots__ = ("K", "V", "k_scale", "v_scale", "refs", "table", "lens", "n_layers", "n_pages", "H_kv", "n_seqs",
-                 "max_pages", "device", "_struct", "_ptr", "_ws_bytes")
+                 "max_pages", "device", "_struct", "_ptr", "_ws_bytes", "_ws")
 
     def __init__(self, K, V, k_scale, v_scale, refs, table, lens):
         if not isinstance(K, torch.Tensor) or K.dim() != 5:
             raise ValueError("K must be a [n_layers, n_pages, H_kv, 64, 64] tensor")
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError("table must be a [n_seqs, max_pages] tensor")
+        if not K.is_cuda:
+            raise ValueError("K must be a CUDA tensor")
         nl, npg, hk = K.shape[:3]
         ns, mp = table.shape
         dev = K.device
@@ -112,6 +131,7 @@ class EntmaxCache:
                                     refs.data_ptr(), table.data_ptr(), lens.data_ptr(), nl, npg, hk, ns, mp)
         self._ptr = ctypes.addressof(self._struct)
         self._ws_bytes = int(lib.entmax_cache_workspace_size(self._ptr))
+        self._ws = {}  # stream handle -> workspace: calls on one stream follow each other
 
     @classmethod
     def new(cls, n_layers: int, n_pages: int, H_kv: int, n_seqs: int, max_pages: int, device="cuda"):
@@ -132,12 +152,22 @@ def _is_cache(cache):
     return cache
 
 
-def _workspace(given, nbytes, device):
-    if given is None:
-        return torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=device)
-    if not isinstance(given, torch.Tensor) or given.device != device or given.numel() * given.element_size() < nbytes:
-        raise ValueError("workspace must be a buffer of at least %d bytes on %s" % (nbytes, device))
-    return given
+def _workspace(cache, given, nbytes, handle):
+    """The caller's workspace, or the cache's own for the stream (kept, and grown where needed).  A call that is being
+    captured gets a buffer of its graph's: graphs captured on one stream may be replayed side by side."""
+    if given is not None:
+        if not isinstance(given, torch.Tensor) or given.device != cache.device \
+                or given.numel() * given.element_size() < nbytes:
+            raise ValueError("workspace must be a buffer of at least %d bytes on %s" % (nbytes, cache.device))
+        return given.data_ptr(), given.numel() * given.element_size()
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=cache.device)
+        return ws.data_ptr(), nbytes
+    kept = cache._ws.get(handle)
+    if kept is None or kept[1] < nbytes:
+        ws = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=cache.device)
+        kept = cache._ws[handle] = (ws.data_ptr(), nbytes, ws)
+    return kept[0], kept[1]
 
 
 def _raise(st, name):
@@ -163,10 +193,10 @@ def entmax_cache_resize(cache, seqs, new_lens, short_pages=None, workspace=None,
             short_pages = torch.empty((1,), dtype=torch.int32, device=c.device)
         else:
             _need("short_pages", short_pages, (1,), torch.int32, c.device)
-        ws = _workspace(workspace, c._ws_bytes, c.device)
-        _raise(lib.entmax_cache_resize(c._ptr, seqs.data_ptr(), new_lens.data_ptr(), n, short_pages.data_ptr(),
-                                       ws.data_ptr(), ws.numel() * ws.element_size(), _handle(stream, c.device)),
-               "entmax_cache_resize")
+        h = _handle(stream, c.device)
+        ws, ws_bytes = _workspace(c, workspace, c._ws_bytes, h)
+        _raise(lib.entmax_cache_resize(c._ptr, seqs.data_ptr(), new_lens.data_ptr(), n, short_pages.data_ptr(), ws,
+                                       ws_bytes, h), "entmax_cache_resize")
     return short_pages
 
 
@@ -190,9 +220,9 @@ def entmax_cache_compact(cache, used=None, workspace=None, stream=None):
             used = torch.empty((1,), dtype=torch.int32, device=c.device)
         else:
             _need("used", used, (1,), torch.int32, c.device)
-        ws = _workspace(workspace, c._ws_bytes, c.device)
-        _raise(lib.entmax_cache_compact(c._ptr, used.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                        _handle(stream, c.device)), "entmax_cache_compact")
+        h = _handle(stream, c.device)
+        ws, ws_bytes = _workspace(c, workspace, c._ws_bytes, h)
+        _raise(lib.entmax_cache_compact(c._ptr, used.data_ptr(), ws, ws_bytes, h), "entmax_cache_compact")
     return used
 
 
@@ -255,11 +285,11 @@ def entmax_cache_attn(cache, layer, Q, seqs, max_len, scale=None, alpha=1.5, out
             tau = torch.empty((n, H), dtype=torch.float32, device=c.device)
         else:
             _need("tau", tau, (n, H), torch.float32, c.device)
-        ws = _workspace(workspace, lib.entmax_cache_attn_workspace_size(n, H, c.H_kv, float(alpha)), c.device)
-        _raise(lib.entmax_cache_attn(c._ptr, int(layer), Q.data_ptr(), qs, seqs.data_ptr(), n, int(max_len),
-                                     float(D ** -0.5 if scale is None else scale), float(alpha), H, O.data_ptr(), code,
-                                     tau.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                     _handle(stream, c.device)), "entmax_cache_attn")
+        h = _handle(stream, c.device)
+        ws, ws_bytes = _workspace(c, workspace, lib.entmax_cache_attn_workspace_size(n, H, c.H_kv, alpha), h)
+        _raise(lib.entmax_cache_attn(c._ptr, layer, Q.data_ptr(), qs, seqs.data_ptr(), n, max_len,
+                                     D ** -0.5 if scale is None else scale, alpha, H, O.data_ptr(), code,
+                                     tau.data_ptr(), ws, ws_bytes, h), "entmax_cache_attn")
     return O, tau
 
 

@@ -65,17 +65,21 @@ struct TokArgs {
 };
 constexpr int GC = 128;      // candidates of a segment and head
 
-// Units of the call and the warps that share them.
+// Units of the call and the warps that share them: each = units / warps of them, the first `more` warps one more.
 struct Deal {
-    long long units;
-    int warps;
-    __device__ __forceinline__ long long start(int w) const { return units * w / warps; }
-    __device__ __forceinline__ int owner(long long u) const { return (int)(((u + 1) * warps - 1) / units); }
+    uint32_t units, warps, each, more;
+    __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ int owner(uint32_t u) const {
+        const uint32_t longer = more * (each + 1);
+        return (int)(u < longer ? u / (each + 1) : more + (u - longer) / each);
+    }
 };
 __device__ __forceinline__ Deal deal_of(const TokArgs& a, int pages) {
     Deal d;
-    d.units = (long long)pages * a.c.Hkv * a.groups;
-    d.warps = (int)min((long long)a.warps, d.units);
+    d.units = (uint32_t)pages * (uint32_t)(a.c.Hkv * a.groups);  // below 2^31: checked for the call's largest
+    d.warps = min((uint32_t)a.warps, d.units);
+    d.each = d.warps ? d.units / d.warps : 0;
+    d.more = d.units - d.each * d.warps;
     return d;
 }
 
@@ -228,9 +232,9 @@ struct Segment {
     long long row;  // i * (H_kv * groups) + its place among the token's rows
 };
 
-__device__ __forceinline__ Segment segment_at(const TokArgs& a, const int* pre, long long u, long long u1) {
-    const int R = a.c.Hkv * a.groups;
-    const long long pg = u / R;  // the row is the last with pre[i] <= pg and at least one page
+__device__ __forceinline__ Segment segment_at(const TokArgs& a, const int* pre, uint32_t u, uint32_t u1) {
+    const uint32_t R = a.c.Hkv * a.groups;
+    const int pg = (int)(u / R);  // the row is the last with pre[i] <= pg and at least one page
     int lo = 0, hi = a.n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -240,10 +244,10 @@ __device__ __forceinline__ Segment segment_at(const TokArgs& a, const int* pre, 
     Segment s;
     s.i = lo;
     s.pages = pre[lo + 1] - pre[lo];
-    const long long rem = u - (long long)pre[lo] * R;
-    const int gr = (int)(rem / s.pages);
-    s.page0 = (int)(rem - (long long)gr * s.pages);
-    s.page1 = (int)min((long long)s.pages, s.page0 + (u1 - u));
+    const uint32_t rem = u - (uint32_t)pre[lo] * R;
+    const int gr = (int)(rem / (uint32_t)s.pages);
+    s.page0 = (int)(rem - (uint32_t)gr * s.pages);
+    s.page1 = (int)min((uint32_t)s.pages, s.page0 + (u1 - u));
     s.row = (long long)lo * R + gr;
     s.kvh = gr / a.groups;
     const int grp = gr - s.kvh * a.groups;
@@ -403,13 +407,13 @@ __global__ void __launch_bounds__(WARPS * 32, 1) token_softmax_kernel(const TokA
     page_prefix<WARPS>(a, pre);
     const Deal deal = deal_of(a, pre[a.n]);
     const int w = warp * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
-    if (w >= deal.warps) return;
+    if (w >= (int)deal.warps) return;
     uint8_t* ring = smem + warp * S_STAGES * S_STAGE_BYTES;
     PageMeta* metas = reinterpret_cast<PageMeta*>(smem + S_META) + warp * S_STAGES;
     const uint32_t ring_u = smem_u32(ring);
 
-    const long long u0 = deal.start(w), u1 = deal.start(w + 1);
-    for (long long u = u0; u < u1;) {
+    const uint32_t u0 = deal.start(w), u1 = deal.start(w + 1);
+    for (uint32_t u = u0; u < u1;) {
         const Segment s = segment_at(a, pre, u, u1);
         uint32_t qf[8];
         const float qinv = load_q(a, s.i, s.head0, s.heads, qf);
@@ -491,7 +495,7 @@ struct RowParts {
     __device__ __forceinline__ size_t slot(int k, int h) const { return ((size_t)(w0 + k) * 2 + (k == 0 ? s0 : 0)) * HG + h; }
 };
 __device__ __forceinline__ RowParts row_parts(const TokArgs& a, const Deal& d, int first_page, int pages, int kvh, int grp) {
-    const long long u = (long long)first_page * a.c.Hkv * a.groups + (long long)(kvh * a.groups + grp) * pages;
+    const uint32_t u = (uint32_t)first_page * (uint32_t)(a.c.Hkv * a.groups) + (uint32_t)(kvh * a.groups + grp) * (uint32_t)pages;
     RowParts r;
     r.w0 = d.owner(u);
     r.w1 = d.owner(u + pages - 1);
@@ -571,7 +575,7 @@ __global__ void __launch_bounds__(JT) token_softmax_join_kernel(const TokArgs a)
 // A page's keys go straight to registers, the next page's under way meanwhile: the fragments are whole
 // 512-byte runs of the block, there are no values to stage, and the shared memory is free for the lists of sixteen
 // warps.  (Through a ring in shared memory with eight warps this kernel took 57 us where it takes SELF.)
-constexpr int E_WARPS = 16;
+constexpr int E_WARPS = 12;
 constexpr int LCAP = 28;   // entries per lane and head
 constexpr int E_KEY = 2 * LCAP * 32 * 4;                        // per warp: float [2][LCAP][32], then u16 [2][LCAP][32]
 constexpr int E_LIST_BYTES = E_KEY + 2 * LCAP * 32 * 2;
@@ -595,7 +599,7 @@ __device__ __forceinline__ float max_g(float v) {
 }
 // A Newton step on sum max(0, s - t)^2 = 4 given its sums: convex and decreasing, so from a lower bound the
 // iterates rise and stay lower bounds.
-__device__ __forceinline__ float newton(float t, float s1, float s2) { return s1 > 0.f ? t + fmaxf(s2 - 4.f, 0.f) / (2.f * s1) : t; }
+__device__ __forceinline__ float newton(float t, float s1, float s2) { return s1 > 0.f ? t + __fdividef(fmaxf(s2 - 4.f, 0.f), 2.f * s1) : t; }
 // A bound less what rounding may have added to it.
 __device__ __forceinline__ float safe(float t) { return t - 2e-6f * fmaxf(1.f, fabsf(t)); }
 
@@ -611,14 +615,17 @@ struct Lists {
         float t0 = cut0, t1 = cut1;
         for (int it = 0; it < steps; ++it) {
             float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
-            for (int e = 0; e < most; ++e) {
-                const float d = e < n0 ? fmaxf(s[e * 32] - t0, 0.f) : 0.f;
-                const float f = e < n1 ? fmaxf(s[(LCAP + e) * 32] - t1, 0.f) : 0.f;
-                a1 += d;
-                a2 = fmaf(d, d, a2);
-                b1 += f;
-                b2 = fmaf(f, f, b2);
-            }
+            for (int e0 = 0; e0 < most; e0 += 4)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int e = e0 + k;  // below LCAP, a multiple of 4
+                    const float d = e < n0 ? fmaxf(s[e * 32] - t0, 0.f) : 0.f;
+                    const float f = e < n1 ? fmaxf(s[(LCAP + e) * 32] - t1, 0.f) : 0.f;
+                    a1 += d;
+                    a2 = fmaf(d, d, a2);
+                    b1 += f;
+                    b2 = fmaf(f, f, b2);
+                }
             t0 = newton(t0, sum_g(a1), sum_g(a2));
             t1 = newton(t1, sum_g(b1), sum_g(b2));
         }
@@ -655,18 +662,18 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
     page_prefix<E_WARPS>(a, pre);
     const Deal deal = deal_of(a, pre[a.n]);
     const int w = warp * gridDim.x + blockIdx.x;
-    if (w >= deal.warps) return;
+    if (w >= (int)deal.warps) return;
     Lists li;
     li.s = reinterpret_cast<float*>(smem + warp * E_LIST_BYTES) + lane;
     li.key = reinterpret_cast<uint16_t*>(smem + warp * E_LIST_BYTES + E_KEY) + lane;
     const int r = key_row(g);
 
-    const long long u0 = deal.start(w), u1 = deal.start(w + 1);
-    for (long long u = u0; u < u1;) {
+    const uint32_t u0 = deal.start(w), u1 = deal.start(w + 1);
+    for (uint32_t u = u0; u < u1;) {
         const Segment s = segment_at(a, pre, u, u1);
         PageRun<false> run;
         run.load(a, s, s.page0);
-        struct Page {
+        struct Page {  // a page under way
             uint4 k[8];  // the lane's 16 bytes of its two keys of each tile
             float ks;
             int valid;
@@ -683,8 +690,8 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
 #pragma unroll
             for (int k = 0; k < 8; ++k) b.k[k] = __ldg(src + 32 * k);
         };
-        Page pa, pb;
-        fetch(s.page0, pa);
+        Page next;
+        fetch(s.page0, next);
         uint32_t qf[8];
         const float qinv = load_q(a, s.i, s.head0, s.heads, qf);
         const float f0 = a.scale * __shfl_sync(0xffffffffu, qinv, 8 * t);
@@ -696,7 +703,9 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
         li.n0 = li.n1 = 0;
         bool odd0 = false, odd1 = false, over0 = false, over1 = false;  // not finite; lists too small
         bool fresh = true;
-        auto process = [&](int p, const Page& b) {
+        for (int p = s.page0; p < s.page1; ++p) {
+            const Page b = next;
+            fetch(p + 1, next);
             float c[4][4], x0 = -INFINITY, x1 = -INFINITY;
             const float h0 = f0 * b.ks, h1 = f1 * b.ks;
 #pragma unroll
@@ -713,67 +722,62 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
                 x0 = max_nan(x0, max_nan(c[mt][0], c[mt][2]));
                 x1 = max_nan(x1, max_nan(c[mt][1], c[mt][3]));
             }
+            const bool end = p + 1 == s.page1;
             // anything above the cuts? (a NaN compares as yes)
-            if (!__any_sync(0xffffffffu, !(x0 <= li.cut0) || !(x1 <= li.cut1))) return;
-            odd0 |= !(x0 < INFINITY);
-            odd1 |= !(x1 < INFINITY);
-            if (fresh && b.valid > 0) {
-                // the first page's own threshold, from its largest score less two
-                fresh = false;
-                float t0 = max_g(x0) - 2.f, t1 = max_g(x1) - 2.f;
-                for (int it = 0; it < 4; ++it) {
-                    float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
+            if (__any_sync(0xffffffffu, !(x0 <= li.cut0) || !(x1 <= li.cut1))) {
+                odd0 |= !(x0 < INFINITY);
+                odd1 |= !(x1 < INFINITY);
+                if (fresh && b.valid > 0) {
+                    // the first page's own threshold, from its largest score less two
+                    fresh = false;
+                    float t0 = max_g(x0) - 2.f, t1 = max_g(x1) - 2.f;
+#pragma unroll 1
+                    for (int it = 0; it < 4; ++it) {
+                        float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
 #pragma unroll
-                    for (int mt = 0; mt < 4; ++mt)
+                        for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                        for (int q = 0; q < 4; q += 2) {
-                            const float d = fmaxf(c[mt][q] - t0, 0.f), e = fmaxf(c[mt][q + 1] - t1, 0.f);
-                            a1 += d;
-                            a2 = fmaf(d, d, a2);
-                            b1 += e;
-                            b2 = fmaf(e, e, b2);
+                            for (int q = 0; q < 4; q += 2) {
+                                const float d = fmaxf(c[mt][q] - t0, 0.f), e = fmaxf(c[mt][q + 1] - t1, 0.f);
+                                a1 += d;
+                                a2 = fmaf(d, d, a2);
+                                b1 += e;
+                                b2 = fmaf(e, e, b2);
+                            }
+                        t0 = newton(t0, sum_g(a1), sum_g(a2));
+                        t1 = newton(t1, sum_g(b1), sum_g(b2));
+                    }
+                    li.cut0 = fmaxf(li.cut0, safe(t0));
+                    li.cut1 = fmaxf(li.cut1, safe(t1));
+                }
+                const int code0 = (p - s.page0) << 3;
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    const bool hit = c[mt][0] > li.cut0 || c[mt][2] > li.cut0 || c[mt][1] > li.cut1 || c[mt][3] > li.cut1;
+                    if (!__any_sync(0xffffffffu, hit)) continue;
+#pragma unroll
+                    for (int q = 0; q < 4; q += 2) {
+                        const uint16_t code = (uint16_t)(code0 + 2 * mt + (q >> 1));
+                        if (c[mt][q] > li.cut0) {
+                            li.s[li.n0 * 32] = c[mt][q];
+                            li.key[li.n0++ * 32] = code;
                         }
-                    t0 = newton(t0, sum_g(a1), sum_g(a2));
-                    t1 = newton(t1, sum_g(b1), sum_g(b2));
-                }
-                li.cut0 = fmaxf(li.cut0, safe(t0));
-                li.cut1 = fmaxf(li.cut1, safe(t1));
-            }
-            const int code0 = (p - s.page0) << 3;
-#pragma unroll
-            for (int mt = 0; mt < 4; ++mt) {
-                const bool hit = c[mt][0] > li.cut0 || c[mt][2] > li.cut0 || c[mt][1] > li.cut1 || c[mt][3] > li.cut1;
-                if (!__any_sync(0xffffffffu, hit)) continue;
-#pragma unroll
-                for (int q = 0; q < 4; q += 2) {
-                    const uint16_t code = (uint16_t)(code0 + 2 * mt + (q >> 1));
-                    if (c[mt][q] > li.cut0) {
-                        li.s[li.n0 * 32] = c[mt][q];
-                        li.key[li.n0++ * 32] = code;
-                    }
-                    if (c[mt][q + 1] > li.cut1) {
-                        li.s[(LCAP + li.n1) * 32] = c[mt][q + 1];
-                        li.key[(LCAP + li.n1++) * 32] = code;
+                        if (c[mt][q + 1] > li.cut1) {
+                            li.s[(LCAP + li.n1) * 32] = c[mt][q + 1];
+                            li.key[(LCAP + li.n1++) * 32] = code;
+                        }
                     }
                 }
             }
-            if (__any_sync(0xffffffffu, max(li.n0, li.n1) > LCAP - 8)) {
+            if (end || __any_sync(0xffffffffu, max(li.n0, li.n1) > LCAP - 8)) {
                 li.prune(4);
-                // still no room for the next page: give the head up
+                // still no room for another page: give the head up
                 over0 |= sum_g(li.n0 > LCAP - 8 ? 1.f : 0.f) > 0.f;
                 over1 |= sum_g(li.n1 > LCAP - 8 ? 1.f : 0.f) > 0.f;
                 if (over0) li.n0 = 0;
                 if (over1) li.n1 = 0;
             }
-        };
-        for (int p = s.page0; p < s.page1; p += 2) {
-            fetch(p + 1, pb);
-            process(p, pa);
-            if (p + 1 >= s.page1) break;
-            fetch(p + 2, pa);
-            process(p + 1, pb);
         }
-        li.prune(6);
         odd0 = sum_g(odd0 ? 1.f : 0.f) > 0.f;
         odd1 = sum_g(odd1 ? 1.f : 0.f) > 0.f;
         // the heads' entries, lanes in order
@@ -1120,7 +1124,9 @@ int entmax_cache_attn(const entmax_cache* c, int layer, const void* Q, long long
     if (!Q || !seqs || !O || !tau || !aligned(Q, 16) || !aligned(seqs, 4) || !aligned(O, 16) || !aligned(tau, 4))
         return ENTMAX_ERR_ARG;
     if (q_stride % 8 || q_stride < 64ll * H) return ENTMAX_ERR_ARG;
-    if ((long long)n * pages_of(max_len) > 0x7fffffffll || (long long)n * H > 0x7fffffffll) return ENTMAX_ERR_UNSUPPORTED;
+    const long long groups = (long long)c->H_kv * ((H / c->H_kv + HG - 1) / HG);
+    if (groups > 0x7fffffffll / n || groups * n > 0x7fffffffll / std::max(pages_of(max_len), 1) || (long long)n * H > 0x7fffffffll)
+        return ENTMAX_ERR_UNSUPPORTED;
     if (!workspace || ws_bytes < ws_bytes_of(n, H, c->H_kv, alpha)) return ENTMAX_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return ENTMAX_ERR_ARG;
     TokArgs a{};
