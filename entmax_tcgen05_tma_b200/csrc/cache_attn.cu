@@ -1007,7 +1007,7 @@ __global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a)
             }
         }
         const float4 s = block_sum4(make_float4(k, s1, s2, 0.f), part);
-        th.step(s.x, s.y, s.z, pass);  // the same in all threads
+        th.step(s.x, s.y, s.z, pass, 5e-3f);  // the same in all threads
         if (th.settled && before) break;
         before = th.settled;
     }

@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <limits.h>
 #include <math.h>
+#include <type_traits>
 #include "../../include/entmax_cache.h"
 #include "common.cuh"
 #include "internal.h"
@@ -264,7 +265,7 @@ __device__ __forceinline__ float first_bound(const float (&top)[TOP], float scal
 
 // Softmax: one pass over the blocks.  1.5-entmax: a pass for the largest scores (the exact threshold of the
 // largest maxima of 32-key chunks is the first bound), passes that sum over the scores above t until every
-// row of both tiles has settled (three as a rule), and the pass that forms P and P V.  S is formed anew in each: the
+// row of both tiles has settled (two or three as a rule), and the pass that forms P and P V.  S is formed anew in each: the
 // tensor core does it in a third of the time that the sums take, and no row is ever too dense for a list.
 template <bool kSoftmax, bool kF32>
 __global__ void __launch_bounds__(PROMPT_THREADS, 1)
@@ -557,18 +558,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 for (int pass = 1; more && live; ++pass) {
                     const uint64_t t2 = f2pack(-th.t, -th.t);
                     uint64_t k2 = 0, s1 = 0, s2 = 0, s3 = 0, s4 = 0;
-                    for (int j = 0; j < nb; ++j) {
-                        float v[4][32];
-                        if (!scores(v, j == nb - 1)) break;
-                        arrive(&ctl->s_read[w]);
+                    const bool count = pass == 1 || pass > 3;  // in between from the passes before
+                    auto sums = [&](const float (&v)[4][32], auto counted) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
 #pragma unroll
                             for (int e = 0; e < 32; e += 2) {
                                 const uint64_t d = f2relu(f2fma(f2pack(v[k][e], v[k][e + 1]), scale2, t2));
-                                float x, y;
-                                f2unpack(d, x, y);
-                                k2 = f2add(k2, f2pack(above0(x), above0(y)));
+                                if (decltype(counted)::value) {
+                                    float x, y;
+                                    f2unpack(d, x, y);
+                                    k2 = f2add(k2, f2pack(above0(x), above0(y)));
+                                }
                                 if (e & 2) {
                                     s1 = f2add(s1, d);
                                     s2 = f2fma(d, d, s2);
@@ -577,6 +578,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                                     s4 = f2fma(d, d, s4);
                                 }
                             }
+                    };
+                    for (int j = 0; j < nb; ++j) {
+                        float v[4][32];
+                        if (!scores(v, j == nb - 1)) break;
+                        arrive(&ctl->s_read[w]);
+                        if (count) sums(v, std::true_type{});
+                        else sums(v, std::false_type{});
                     }
                     n_kv += nb_all;
                     if (!live) break;
@@ -585,7 +593,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         f2unpack(k2, kx, ky);
                         f2unpack(f2add(s1, s3), x0, x1);
                         f2unpack(f2add(s2, s4), y0, y1);
-                        th.step(kx + ky, x0 + x1, y0 + y1, pass);
+                        th.step(count ? kx + ky : -1.f, x0 + x1, y0 + y1, pass, kF32 ? 5e-3f : 0.02f);
                     }
                     const bool any = __any_sync(0xffffffffu, !th.settled && pass < MOST_PASSES);
                     if (lane == 0) {
@@ -601,7 +609,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             // the pass that forms P: softmax weights on the way to the running reference m, or 1.5-entmax weights
             // at the threshold found
             float m = -INFINITY;
-            uint64_t l2 = 0, l3 = 0;
+            uint64_t l2 = 0, l3 = 0, x2 = 0;  // sums of P, and for 1.5-entmax of sqrt(P)
             const float half = 0.5f * a.scale, t_half = -0.5f * th.t;
             const uint64_t t2 = f2pack(t_half, t_half), h2 = f2pack(half, half), c2 = f2pack(c, c);
             for (int j = 0; j < nb; ++j) {
@@ -652,16 +660,15 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         uint64_t p;
                         if (!kSoftmax) {
                             p = f2relu(f2fma(x, h2, t2));
+                            x2 = f2add(x2, p);
                             p = f2mul(p, p);
                         } else {
                             float x0, x1;
                             f2unpack(f2fma(x, c2, off2), x0, x1);
                             p = f2pack(ex2(x0), ex2(x1));
                         }
-                        if (kSoftmax) {
-                            if (e & 2) l3 = f2add(l3, p);
-                            else l2 = f2add(l2, p);
-                        }
+                        if (e & 2) l3 = f2add(l3, p);
+                        else l2 = f2add(l2, p);
                         if (kF32) {
                             f2split3(p, hi[e >> 1], mid[e >> 1], lo[e >> 1]);
                         } else {
@@ -711,13 +718,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 tmem_wait_ld(o[0]);
                 tmem_wait_ld(o[1]);
                 arrive(&ctl->o_empty[w]);
-                float inv = odd ? NAN : 1.f, tau = odd ? NAN : th.t;
+                float x0, x1;
+                f2unpack(f2add(l2, l3), x0, x1);
+                const float l = x0 + x1;
+                float inv = odd ? NAN : 1.f, tau = NAN;
                 if (kSoftmax) {
-                    float x0, x1;
-                    f2unpack(f2add(l2, l3), x0, x1);
-                    const float l = x0 + x1;
                     inv = 1.f / l;
                     tau = (m * c + log2f(l)) * LN2_F;
+                } else if (!odd) {  // a last Newton step on sum P = 1: what is left of tau's error squared
+                    f2unpack(x2, x0, x1);
+                    tau = th.t + (l - 1.f) / (x0 + x1);
                 }
                 if (i < it.len) {
                     const size_t t = (size_t)(it.first + i);
