@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(PT) resize_kernel(const CacheArgs c, const int
     __shared__ int part[32];
     __shared__ int any_shared;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    let_next_start();
     if (tid == 0) {
         *ws.count = 0;
         any_shared = 0;
@@ -261,9 +262,9 @@ __global__ void __launch_bounds__(PT) resize_kernel(const CacheArgs c, const int
 // H_kv * 4 KB in one piece.  Bound by HBM: 16 KB pieces, 64 bytes in flight per thread.  kRenumber: the
 // pages moved, so table entries that name map[p] >= 0 follow (compact).
 template <bool kRenumber>
-__global__ void __launch_bounds__(256) copy_pages_kernel(const CacheArgs c, const int* __restrict__ src,
-                                                         const int* __restrict__ dst, const int* __restrict__ count,
-                                                         const int* __restrict__ map) {
+__global__ void __launch_bounds__(256) copy_pages_kernel(const CacheArgs c, const int* src, const int* dst, const int* count,
+                                                         const int* map) {
+    wait_for_previous();
     const int n = *count;
     if (kRenumber) {
         const size_t cells = (size_t)c.n_seqs * c.max_pages;
@@ -309,6 +310,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const CacheArgs c, cons
 __global__ void __launch_bounds__(PT) compact_plan_kernel(const CacheArgs c, int* used_out, const PageWs ws) {
     __shared__ int part[32];
     const int tid = threadIdx.x;
+    let_next_start();
     int mine = 0;
     for (int p = tid; p < c.n_pages; p += PT) mine += c.refs[p] > 0 ? 1 : 0;
     int used;
@@ -571,8 +573,7 @@ int entmax_cache_resize(const entmax_cache* c, const int32_t* seqs, const int32_
     resize_kernel<<<1, PT, smem, stream>>>(a, seqs, new_lens, n, short_pages, ws);
     rc = abi_record(cudaGetLastError());
     if (rc || n == 0) return rc;
-    copy_pages_kernel<false><<<COPY_GRID, 256, 0, stream>>>(a, ws.pairs, ws.pairs + MAX_LIST, ws.count, nullptr);
-    return abi_record(cudaGetLastError());
+    return abi_record(launch_next(copy_pages_kernel<false>, COPY_GRID, 256, stream, a, ws.pairs, ws.pairs + MAX_LIST, ws.count, nullptr));
 }
 
 int entmax_cache_fork(const entmax_cache* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream) {
@@ -596,8 +597,7 @@ int entmax_cache_compact(const entmax_cache* c, int32_t* used, void* workspace, 
     compact_plan_kernel<<<1, PT, 0, stream>>>(a, used, ws);
     rc = abi_record(cudaGetLastError());
     if (rc) return rc;
-    copy_pages_kernel<true><<<COPY_GRID, 256, 0, stream>>>(a, ws.a, ws.b, ws.count, ws.c);
-    return abi_record(cudaGetLastError());
+    return abi_record(launch_next(copy_pages_kernel<true>, COPY_GRID, 256, stream, a, ws.a, ws.b, ws.count, ws.c));
 }
 
 int entmax_cache_append(const entmax_cache* c, int layer, const void* K, long long k_stride, const void* V,

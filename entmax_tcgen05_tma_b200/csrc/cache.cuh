@@ -33,6 +33,24 @@ int cache_args(const entmax_cache* c, CacheArgs* out);
 __device__ __forceinline__ void cache_error(const CacheArgs& c) { atomicExch(c.status, STATUS_ARG); }
 __host__ __device__ __forceinline__ int pages_of(int tokens) { return (int)(((unsigned)tokens + PAGE - 1) / PAGE); }
 
+// Two kernels of one call: the first lets the second's CTAs start early (no more than their launch is early: they
+// wait for its end before they read anything), which hides the second launch.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... P, class... A>
+cudaError_t launch_next(void (*f)(P...), unsigned grid, unsigned threads, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, f, static_cast<P>(args)...);
+}
+
 // Two e4m3 numbers (low byte first) as two fp16 numbers: exact, NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
     uint32_t r;

@@ -404,6 +404,7 @@ __global__ void __launch_bounds__(WARPS * 32, 1) token_softmax_kernel(const TokA
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int* pre = reinterpret_cast<int*>(smem + S_PRE);
+    let_next_start();
     page_prefix<WARPS>(a, pre);
     const Deal deal = deal_of(a, pre[a.n]);
     const int w = warp * gridDim.x + blockIdx.x;  // neighbouring runs on different SMs
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(JT) token_softmax_join_kernel(const TokArgs a)
     __shared__ float maxs[4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x / a.H, head = blockIdx.x - i * a.H;
+    wait_for_previous();
     const int first = a.prefix[i], pages = a.prefix[i + 1] - first;
     const size_t row = (size_t)i * a.H + head;
     if (pages == 0) {  // an empty sequence
@@ -659,6 +661,7 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     int* pre = reinterpret_cast<int*>(smem + E_PRE);
+    let_next_start();
     page_prefix<E_WARPS>(a, pre);
     const Deal deal = deal_of(a, pre[a.n]);
     const int w = warp * gridDim.x + blockIdx.x;
@@ -856,6 +859,7 @@ __global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a)
     __shared__ const uint8_t* vat[EJT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x / a.H, head = blockIdx.x - i * a.H;
+    wait_for_previous();
     const int first = a.prefix[i], pages = a.prefix[i + 1] - first;
     const size_t row = (size_t)i * a.H + head;
     auto put = [&](float fill, float tau) {  // a row without weights
@@ -1170,9 +1174,8 @@ int entmax_cache_attn(const entmax_cache* c, int layer, const void* Q, long long
     else token_entmax_kernel<<<GRID, E_WARPS * 32, entmax_smem(n), stream>>>(a);
     rc = abi_record(cudaGetLastError());
     if (rc) return rc;
-    if (soft) token_softmax_join_kernel<<<n * H, JT, 0, stream>>>(a);
-    else token_entmax_join_kernel<<<n * H, EJT, 0, stream>>>(a);
-    return abi_record(cudaGetLastError());
+    return abi_record(soft ? launch_next(token_softmax_join_kernel, n * H, JT, stream, a)
+                           : launch_next(token_entmax_join_kernel, n * H, EJT, stream, a));
 }
 
 }  // extern "C"

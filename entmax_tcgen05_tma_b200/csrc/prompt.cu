@@ -75,7 +75,7 @@ constexpr int PROMPT_SMEM = O_CTL + (int)sizeof(Ctl) + 1024;
 static_assert(PROMPT_SMEM <= 227 * 1024, "shared memory");
 // while the work list is made, the ring holds the sequences' pair counts and the counts by size
 constexpr int LOADS_AT = MAX_SEQS + 2 * (MAX_PAIRS + 2);
-static_assert(LOADS_AT % 4 == 0 && GRID % 4 == 0 && (LOADS_AT + GRID + LIST) * 4 <= NS * 2 * BLOCK16, "list scratch");
+static_assert(LOADS_AT % 4 == 0 && GRID % 4 == 0 && (LOADS_AT + (1 + BALANCED) * GRID + LIST) * 4 <= NS * 2 * BLOCK16, "list scratch");
 // TMEM columns: S of tile w at 128 w, O at 256 + 64 w, P at 384 + 64 w, so that S of the next block is formed while
 // this block's P is.  Three parts do not fit beside S: the first two then lie over S, and the third at P's place.
 constexpr int TM_S = 0, TM_O = 256, TM_P = 384;
@@ -180,6 +180,7 @@ __device__ __forceinline__ void make_list(const AttnArgs& a, long long first_ite
     // turns; over more, turns that change direction are as even)
     int* load = scratch + LOADS_AT;      // [GRID], multiples of GRID plus the CTA's number: no two are alike
     int* my_place = load + GRID;         // [turns] place of this CTA in the turn
+    int* sizes = my_place + LIST;        // [BALANCED][G]
     auto pair_of = [&](int k) {          // the highest t with before[t] + more[t] > k
         int lo = 0, hi = P;
         while (hi - lo > 1) {
@@ -191,26 +192,27 @@ __device__ __forceinline__ void make_list(const AttnArgs& a, long long first_ite
     };
     if (turns <= BALANCED) {
         for (int k = tid; k < GRID; k += PROMPT_THREADS) load[k] = k < G ? k : INT_MAX;
+        for (int k = tid; k < turns * G; k += PROMPT_THREADS) {  // about half the blocks of every item, and its fixed cost
+            const long long at = first_item + k;
+            sizes[k] = at < total ? 2 * pair_of((int)(at / a.H)) + 3 : 0;
+        }
         __syncthreads();
         for (int q = 0; q < turns; ++q) {
-            int place = 0, size = 0;
-            if (tid < G) {
+            int place = tid;
+            if (tid < G && q > 0) {
                 const int mine = load[tid];
-                if (q == 0) {
-                    place = tid;
-                } else {
+                place = 0;
 #pragma unroll
-                    for (int k = 0; k < GRID / 4; ++k) {
-                        const int4 x = reinterpret_cast<const int4*>(load)[k];
-                        place += (x.x < mine) + (x.y < mine) + (x.z < mine) + (x.w < mine);
-                    }
+                for (int k = 0; k < GRID / 4; ++k) {
+                    const int4 x = reinterpret_cast<const int4*>(load)[k];
+                    place += (x.x < mine) + (x.y < mine) + (x.z < mine) + (x.w < mine);
                 }
-                const long long at = first_item + (long long)q * G + place;
-                if (at < total) size = 2 * pair_of((int)(at / a.H)) + 3;  // about half its blocks, and its fixed cost
-                if (tid == blockIdx.x) my_place[q] = place;
             }
             __syncthreads();
-            if (tid < G) load[tid] += size * GRID;
+            if (tid < G) {
+                load[tid] += sizes[q * G + place] * GRID;
+                if (tid == blockIdx.x) my_place[q] = place;
+            }
             __syncthreads();
         }
     } else {
