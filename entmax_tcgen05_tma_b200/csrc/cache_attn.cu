@@ -91,8 +91,8 @@ __device__ __forceinline__ int row_len(const TokArgs& a, int i) {
     return len < 0 || len > a.max_len ? -1 : len;
 }
 
-// Exclusive prefix of the rows' page counts into pre[0 .. n] (whole CTA); CTA 0 leaves it in the workspace
-// and reports rows out of range.
+// Exclusive prefix of the rows' page counts into pre[0 .. n] and the rows' lengths behind it (whole CTA); CTA 0
+// leaves the prefix in the workspace and reports rows out of range.
 template <int kWarps>
 __device__ __forceinline__ void page_prefix(const TokArgs& a, int* pre) {
     __shared__ int part[kWarps];
@@ -121,6 +121,7 @@ __device__ __forceinline__ void page_prefix(const TokArgs& a, int* pre) {
         }
         if (i < a.n) {
             pre[i] = before + x - v;
+            pre[a.n + 1 + i] = max(len, 0);
             if (blockIdx.x == 0) a.prefix[i] = before + x - v;
         }
         carry += all;
@@ -180,14 +181,16 @@ __device__ __forceinline__ void load_block(uint32_t dst, const uint8_t* src, int
 
 // Fragments of q for a group's heads: lane (g, t) holds head g's dimensions 16 t .. 16 t + 15 as fp16 times a
 // power of two; returns that power's inverse.  Heads at or past `heads` are zero.
-__device__ __forceinline__ float load_q(const TokArgs& a, int i, int head0, int heads, uint32_t (&qf)[8]) {
+__device__ __forceinline__ void fetch_q(const TokArgs& a, int i, int head0, int heads, uint4 (&x)[2]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    uint4 x[2] = {};
+    x[0] = x[1] = make_uint4(0, 0, 0, 0);
     if (g < heads) {
         const uint4* src = reinterpret_cast<const uint4*>(a.Q + (long long)i * a.q_stride + (head0 + g) * 64 + 16 * t);
         x[0] = __ldg(src);
         x[1] = __ldg(src + 1);
     }
+}
+__device__ __forceinline__ float scale_q(const uint4 (&x)[2], uint32_t (&qf)[8]) {
     const uint32_t w[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
     uint32_t m = 0;
 #pragma unroll
@@ -254,7 +257,7 @@ __device__ __forceinline__ Segment segment_at(const TokArgs& a, const int* pre, 
     s.head0 = s.kvh * a.G + grp * HG;
     s.heads = min(HG, a.G - grp * HG);
     s.seq = a.seqs[lo];
-    s.len = a.c.lens[s.seq];
+    s.len = pre[a.n + 1 + lo];
     return s;
 }
 
@@ -293,7 +296,8 @@ struct PageMeta {
 constexpr int S_RING = WARPS * S_STAGES * S_STAGE_BYTES;
 constexpr int S_META = S_RING;
 constexpr int S_PRE = S_META + WARPS * S_STAGES * (int)sizeof(PageMeta);
-constexpr int softmax_smem(int n) { return S_PRE + (n + 1) * 4; }
+constexpr int softmax_smem(int n) { return S_PRE + (2 * n + 1) * 4; }
+static_assert(softmax_smem(MAX_TOKENS) <= 226 * 1024, "shared memory");
 
 // One page's share of O and of the sums.  kPart: the page holds fewer than 64 keys (rows behind the end may
 // hold anything).
@@ -416,13 +420,15 @@ __global__ void __launch_bounds__(WARPS * 32, 1) token_softmax_kernel(const TokA
     const uint32_t u0 = deal.start(w), u1 = deal.start(w + 1);
     for (uint32_t u = u0; u < u1;) {
         const Segment s = segment_at(a, pre, u, u1);
+        uint4 qx[2];
+        fetch_q(a, s.i, s.head0, s.heads, qx);
+        PageRun<true> run;
+        run.load(a, s, s.page0);
         uint32_t qf[8];
-        const float qinv = load_q(a, s.i, s.head0, s.heads, qf);
+        const float qinv = scale_q(qx, qf);
         // x = S log2 e = raw * f for the lane's two heads
         const float f0 = a.scale * LOG2E_F * __shfl_sync(0xffffffffu, qinv, 8 * t);
         const float f1 = a.scale * LOG2E_F * __shfl_sync(0xffffffffu, qinv, 8 * t + 4);
-        PageRun<true> run;
-        run.load(a, s, s.page0);
         auto fetch = [&](int p) {  // page p of the segment into its stage
             if (p < s.page1) {
                 if (p >= run.base + 32) run.load(a, s, p);
@@ -583,7 +589,7 @@ constexpr int E_KEY = 2 * LCAP * 32 * 4;                        // per warp: flo
 constexpr int E_LIST_BYTES = E_KEY + 2 * LCAP * 32 * 2;
 constexpr int E_PRE = E_WARPS * E_LIST_BYTES;
 constexpr int E_MAX_LEN = 8192 * PAGE;                          // an entry's key: 13 bits page of the segment, 3 bits place
-constexpr int entmax_smem(int n) { return E_PRE + (n + 1) * 4; }
+constexpr int entmax_smem(int n) { return E_PRE + (2 * n + 1) * 4; }
 static_assert(entmax_smem(MAX_TOKENS) <= 226 * 1024, "shared memory");
 
 // Sum over the eight lanes that hold one head.
@@ -615,41 +621,35 @@ struct Lists {
     __device__ __forceinline__ void prune(int steps) {
         const int most = __reduce_max_sync(0xffffffffu, max(n0, n1));
         float t0 = cut0, t1 = cut1;
+#pragma unroll 1
         for (int it = 0; it < steps; ++it) {
             float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
-            for (int e0 = 0; e0 < most; e0 += 4)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int e = e0 + k;  // below LCAP, a multiple of 4
-                    const float d = e < n0 ? fmaxf(s[e * 32] - t0, 0.f) : 0.f;
-                    const float f = e < n1 ? fmaxf(s[(LCAP + e) * 32] - t1, 0.f) : 0.f;
-                    a1 += d;
-                    a2 = fmaf(d, d, a2);
-                    b1 += f;
-                    b2 = fmaf(f, f, b2);
-                }
+#pragma unroll 2
+            for (int e = 0; e < most; ++e) {
+                const float d = e < n0 ? fmaxf(s[e * 32] - t0, 0.f) : 0.f;
+                const float f = e < n1 ? fmaxf(s[(LCAP + e) * 32] - t1, 0.f) : 0.f;
+                a1 += d;
+                a2 = fmaf(d, d, a2);
+                b1 += f;
+                b2 = fmaf(f, f, b2);
+            }
             t0 = newton(t0, sum_g(a1), sum_g(a2));
             t1 = newton(t1, sum_g(b1), sum_g(b2));
         }
         cut0 = fmaxf(cut0, safe(t0));
         cut1 = fmaxf(cut1, safe(t1));
         int k0 = 0, k1 = 0;
+#pragma unroll 1
         for (int e = 0; e < most; ++e) {
-            if (e < n0) {
-                const float x = s[e * 32];
-                const uint16_t y = key[e * 32];
-                if (x > cut0) {
-                    s[k0 * 32] = x;
-                    key[k0++ * 32] = y;
-                }
+            const float x0 = s[e * 32], x1 = s[(LCAP + e) * 32];
+            const uint16_t y0 = key[e * 32], y1 = key[(LCAP + e) * 32];
+            if (e < n0 && x0 > cut0) {
+                s[k0 * 32] = x0;
+                key[k0++ * 32] = y0;
             }
-            if (e < n1) {
-                const float x = s[(LCAP + e) * 32];
-                const uint16_t y = key[(LCAP + e) * 32];
-                if (x > cut1) {
-                    s[(LCAP + k1) * 32] = x;
-                    key[(LCAP + k1++) * 32] = y;
-                }
+            if (e < n1 && x1 > cut1) {
+                s[(LCAP + k1) * 32] = x1;
+                key[(LCAP + k1++) * 32] = y1;
             }
         }
         n0 = k0;
@@ -674,6 +674,8 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
     const uint32_t u0 = deal.start(w), u1 = deal.start(w + 1);
     for (uint32_t u = u0; u < u1;) {
         const Segment s = segment_at(a, pre, u, u1);
+        uint4 qx[2];
+        fetch_q(a, s.i, s.head0, s.heads, qx);
         PageRun<false> run;
         run.load(a, s, s.page0);
         struct Page {  // a page under way
@@ -696,7 +698,7 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
         Page next;
         fetch(s.page0, next);
         uint32_t qf[8];
-        const float qinv = load_q(a, s.i, s.head0, s.heads, qf);
+        const float qinv = scale_q(qx, qf);
         const float f0 = a.scale * __shfl_sync(0xffffffffu, qinv, 8 * t);
         const float f1 = a.scale * __shfl_sync(0xffffffffu, qinv, 8 * t + 4);
         // a head that the group does not have takes nothing
@@ -735,7 +737,7 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
                     fresh = false;
                     float t0 = max_g(x0) - 2.f, t1 = max_g(x1) - 2.f;
 #pragma unroll 1
-                    for (int it = 0; it < 4; ++it) {
+                    for (int it = 0; it < 3; ++it) {
                         float a1 = 0.f, a2 = 0.f, b1 = 0.f, b2 = 0.f;
 #pragma unroll
                         for (int mt = 0; mt < 4; ++mt)
@@ -773,7 +775,7 @@ __global__ void __launch_bounds__(E_WARPS * 32, 1) token_entmax_kernel(const Tok
                 }
             }
             if (end || __any_sync(0xffffffffu, max(li.n0, li.n1) > LCAP - 8)) {
-                li.prune(4);
+                li.prune(3);
                 // still no room for another page: give the head up
                 over0 |= sum_g(li.n0 > LCAP - 8 ? 1.f : 0.f) > 0.f;
                 over1 |= sum_g(li.n1 > LCAP - 8 ? 1.f : 0.f) > 0.f;
@@ -847,7 +849,7 @@ __device__ __forceinline__ float4 e4m3x4_to_f32(uint32_t v) {
     return make_float4(a.x, a.y, b.x, b.y);
 }
 
-__global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a) {
+__global__ void __launch_bounds__(EJT, 4) token_entmax_join_kernel(const TokArgs a) {
     __shared__ float2 ent[JCAP];
     __shared__ float4 part[EJ_WARPS];
     __shared__ float qs[64];
@@ -857,6 +859,7 @@ __global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a)
     __shared__ short seg_n[GRID * E_WARPS];
     __shared__ float wts[EJT];
     __shared__ const uint8_t* vat[EJT];
+    __shared__ int vkey[EJT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i = blockIdx.x / a.H, head = blockIdx.x - i * a.H;
     wait_for_previous();
@@ -942,27 +945,30 @@ __global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a)
         return acc * a.c.ks[blk];
     };
     if (least == 0) {
-        // sixteen segments a step and warp, eight lanes a segment
-        const int sub = lane >> 3, le = lane & 7;
+        // sixteen segments a step and warp, sixteen lanes a segment: as a rule all of its entries
+        const int sub = lane >> 4, le = lane & 15;
         for (int k0 = warp * 16; k0 < segs; k0 += EJ_WARPS * 16) {
-            float2 x[4];
-            int n[4];
+            float2 x[8];
+            int n[8], most = 0;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int k = k0 + 4 * q + sub;
+            for (int q = 0; q < 8; ++q) {
+                const int k = k0 + 2 * q + sub;
                 n[q] = k < segs ? seg_n[k] : 0;
+                most = max(most, n[q]);
                 x[q] = make_float2(-INFINITY, 0.f);
                 if (le < n[q]) x[q] = a.cand[(slot0 + (size_t)k * a.heads) * GC + le];
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                append(x[q]);
-                const int most = __reduce_max_sync(0xffffffffu, n[q]);
-                for (int e = 8 + le; e - le < most; e += 8) {
-                    float2 y = make_float2(-INFINITY, 0.f);
-                    if (e < n[q]) y = a.cand[(slot0 + (size_t)(k0 + 4 * q + sub) * a.heads) * GC + e];
-                    append(y);
+            for (int q = 0; q < 8; ++q) append(x[q]);
+            most = __reduce_max_sync(0xffffffffu, most);
+            for (int e = 16 + le; e - le < most; e += 16) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    x[q] = make_float2(-INFINITY, 0.f);
+                    if (e < n[q]) x[q] = a.cand[(slot0 + (size_t)(k0 + 2 * q + sub) * a.heads) * GC + e];
                 }
+#pragma unroll
+                for (int q = 0; q < 8; ++q) append(x[q]);
             }
         }
     } else {
@@ -1000,6 +1006,35 @@ __global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a)
     Threshold th;
     th.start(cut);
     bool before = false;  // one pass beyond the settled one: it costs little here, and leaves nothing of the error
+    if (listed && count <= 8 * 32) {
+        // every warp by itself, all alike: eight entries a lane, no barriers
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int j = lane + 32 * k;
+            x[k] = j < count ? ent[place(j)].x : -INFINITY;
+        }
+#pragma unroll 1
+        for (int pass = 1; pass <= MOST_PASSES; ++pass) {
+            float k0 = 0.f, s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float d = fmaxf(x[k] - th.t, 0.f);
+                k0 += d > 0.f ? 1.f : 0.f;
+                s1 += d;
+                s2 = fmaf(d, d, s2);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                k0 += __shfl_xor_sync(0xffffffffu, k0, o);
+                s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+                s2 += __shfl_xor_sync(0xffffffffu, s2, o);
+            }
+            th.step(k0, s1, s2, pass, 5e-3f);
+            if (th.settled && before) break;
+            before = th.settled;
+        }
+    } else
     for (int pass = 1; pass <= MOST_PASSES; ++pass) {
         float k = 0.f, s1 = 0.f, s2 = 0.f;
         for (int j = tid; j < count; j += EJT) {
@@ -1016,40 +1051,16 @@ __global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a)
         before = th.settled;
     }
     const float t = th.t;
-    // O = sum p_j V_j.  Weights and places of up to EJT keys at a time in shared memory, then groups of 16 lanes, a
-    // key each, four dimensions a lane
+    // O = sum p_j V_j.  The support's depths and keys in batches of at most EJT, then their weights and places, then
+    // groups of 16 lanes, a key each, four dimensions a lane
     const int grp16 = tid >> 4, l16 = tid & 15;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < count; j0 += EJT) {
-        const int j = j0 + tid;
-        float w = 0.f;
-        const uint8_t* va = a.c.V;
-        if (j < count) {
-            float2 x = make_float2(0.f, __int_as_float(j));
-            if (listed) x = ent[place(j)];
-            else x.x = score(j);
-            const float e = x.x - t;
-            if (e > 0.f) {
-                const int key = __float_as_int(x.y);
-                const size_t blk = a.c.block(a.layer, table[key / PAGE], kvh);
-                w = 0.25f * e * e * a.c.vs[blk];
-                va += blk * BLOCK_BYTES + (key % PAGE) * 64;
-            }
-        }
-        // the keys of the support to the front, in order
-        const uint32_t keep = __ballot_sync(0xffffffffu, w != 0.f);
-        __syncthreads();  // the batch before is read
-        if (lane == 0) counts[warp] = __popc(keep);
-        __syncthreads();
-        int to = __popc(keep & ((1u << lane) - 1u)), m = 0;
-#pragma unroll
-        for (int v = 0; v < EJ_WARPS; ++v) {
-            if (v < warp) to += counts[v];
-            m += counts[v];
-        }
-        if (w != 0.f) {
-            wts[to] = w;
-            vat[to] = va;
+    auto add_batch = [&](int m) {  // wts[k], vkey[k]: depth and key of the batch's m entries; whole CTA
+        if (tid < m) {
+            const int key = vkey[tid];
+            const size_t blk = a.c.block(a.layer, table[key / PAGE], kvh);
+            vat[tid] = a.c.V + blk * BLOCK_BYTES + (key % PAGE) * 64;
+            wts[tid] = 0.25f * wts[tid] * wts[tid] * a.c.vs[blk];
         }
         __syncthreads();
 #pragma unroll 4
@@ -1061,7 +1072,39 @@ __global__ void __launch_bounds__(EJT) token_entmax_join_kernel(const TokArgs a)
             o.z = fmaf(p, v.z, o.z);
             o.w = fmaf(p, v.w, o.w);
         }
+        __syncthreads();
+    };
+    int have = 0;  // entries of the batch so far, the same in all threads
+    for (int j0 = 0; j0 < count; j0 += EJT) {
+        const int j = j0 + tid;
+        float2 x = make_float2(-INFINITY, __int_as_float(j));
+        if (j < count) {
+            if (listed) x = ent[place(j)];
+            else x.x = score(j);
+        }
+        const bool in_it = x.x > t;
+        const uint32_t keep = __ballot_sync(0xffffffffu, in_it);
+        if (lane == 0) counts[warp] = __popc(keep);
+        __syncthreads();
+        int before = 0, m = 0;
+#pragma unroll
+        for (int v = 0; v < EJ_WARPS; ++v) {
+            if (v < warp) before += counts[v];
+            m += counts[v];
+        }
+        if (have + m > EJT) {
+            add_batch(have);
+            have = 0;
+        }
+        if (in_it) {
+            const int to = have + before + __popc(keep & ((1u << lane) - 1u));
+            wts[to] = x.x - t;
+            vkey[to] = __float_as_int(x.y);
+        }
+        have += m;
+        __syncthreads();  // written, and the counts are read
     }
+    if (have > 0) add_batch(have);
     osum[grp16][l16] = o;
     __syncthreads();
     if (tid < 16) {

@@ -36,17 +36,21 @@ struct Threshold {
         }
         if (k < 0.f) {
             const float mean_k = t != t_before ? __fdividef(s1_before - s1, t - t_before) : k_before;
-            k = fmaxf(2.f * mean_k - k_before, s1 * s1 / s2);  // at least that, by Cauchy and Schwarz
+            k = fmaxf(2.f * mean_k - k_before, __fdividef(s1 * s1, s2));  // at least that, by Cauchy and Schwarz
         }
         t_before = t;
         s1_before = s1;
         k_before = k;
-        lo = fmaxf(lo, t + (s2 - 4.f) / (2.f * s1));
-        const float mean = s1 / k, rest = 4.f / k - (s2 / k - mean * mean);
-        const float root = t + mean - sqrtf(fmaxf(rest, 0.f));
+        // quotients and the root to about 2^-22: a few instructions each, in code that mostly runs once a row
+        const float per_s1 = __fdividef(1.f, s1), per_k = __fdividef(1.f, k);
+        lo = fmaxf(lo, t + 0.5f * (s2 - 4.f) * per_s1);
+        const float mean = s1 * per_k, rest = (4.f - s2) * per_k + mean * mean;
+        float root;
+        asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(fmaxf(rest, 0.f)));
+        root = t + mean - root;
         const bool closed = rest >= 0.f && root >= lo && pass <= CLOSED;
         const float next = closed ? root : lo;
-        settled = !(fabsf(next - t) > (closed ? step : STEP_NEWTON) * (s2 / s1));
+        settled = !(fabsf(next - t) > (closed ? step : STEP_NEWTON) * s2 * per_s1);
         t = next;
     }
 };
