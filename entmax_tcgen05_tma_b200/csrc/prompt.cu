@@ -399,7 +399,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             const uint32_t ring_u = __shfl_sync(0xffffffffu, smem_u32(ring), 0);
             const uint32_t q_u = __shfl_sync(0xffffffffu, smem_u32(sQ), 0) + w * TILE_BYTES;
             const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t s_tm = tm + TM_S + 128u * w, o_tm = tm + TM_O + 64u * w, p_tm = kF32 ? s_tm : tm + TM_P + 64u * w;
+            const uint32_t s_tm = tm + TM_S + 128u * w, o_tm = tm + TM_O + 64u * w;
             const int n_items = __shfl_sync(0xffffffffu, items, 0);
             for (int q = 0; q < n_items && ok; ++q) {
                 const Item it = list[q];
@@ -445,16 +445,13 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                             const uint64_t vm = umma_desc_mnmajor_sw128(ring_u + pst * 2 * BLOCK16 + BLOCK16);
                             if (leader) {
 #pragma unroll
-                                for (int k = 0; k < KB / 16; ++k)
-                                    tc_mma_bf16_ta(o_tm, p_tm + 8 * k, vm + 128u * k, IDESC_O, (j > 1 || k > 0) ? 1u : 0u);
-                                if (kF32) {
+                                for (int part = kF32 ? 2 : 0; part >= 0; --part)  // the smallest part first
 #pragma unroll
-                                    for (int k = 0; k < KB / 16; ++k)
-                                        tc_mma_bf16_ta(o_tm, p_tm + 64 + 8 * k, vm + 128u * k, IDESC_O, 1u);
-#pragma unroll
-                                    for (int k = 0; k < KB / 16; ++k)
-                                        tc_mma_bf16_ta(o_tm, tm + TM_P + 64u * w + 8 * k, vm + 128u * k, IDESC_O, 1u);
-                                }
+                                    for (int k = 0; k < KB / 16; ++k) {
+                                        const uint32_t at = !kF32 || part == 2 ? tm + TM_P + 64u * w + 8 * k : s_tm + 16 * k + 8 * part;
+                                        tc_mma_bf16_ta(o_tm, at, vm + 128u * k, IDESC_O,
+                                                       (kF32 ? part < 2 || k > 0 : j > 1 || k > 0) ? 1u : 0u);
+                                    }
                             }
                             commit(&ctl->p_empty[w], (uint32_t)np & 1u);
                             ++np;
@@ -493,7 +490,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         const int w = warp >> 2, r = tid & (TILE - 1);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t s_tm = tmem + lanes + TM_S + 128u * w, o_tm = tmem + lanes + TM_O + 64u * w;
-        const uint32_t p_tm = kF32 ? s_tm : tmem + lanes + TM_P + 64u * w;
+        const uint32_t p_tm = tmem + lanes + TM_P + 64u * w;
         const float c = a.scale * LOG2E_F, raise = RAISE / c;
         const uint64_t scale2 = f2pack(a.scale, a.scale);
         int ns = 0, np = 0, no = 0, n_kv = 0, n_vote = 0;
@@ -508,7 +505,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(bar));
         };
-        // the scores of the tile's next block, keys behind the row at -inf in its last one
+        auto hide = [&](auto& x, int first) {  // keys behind the row to -inf
+#pragma unroll
+            for (int e = 0; e < (int)(sizeof(x) / sizeof(x[0])); ++e)
+                if (first + e > r) x[e] = -INFINITY;
+        };
+        // the scores of the tile's next block
         auto scores = [&](float (&v)[4][32], bool diag) -> bool {
             if (!wait(&ctl->s_full[w], (uint32_t)ns & 1u)) return false;
             ++ns;
@@ -519,10 +521,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             for (int k = 0; k < 4; ++k) tmem_wait_ld(v[k]);
             if (diag)
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * k + e > r) v[k][e] = -INFINITY;
+                for (int k = 0; k < 4; ++k) hide(v[k], 32 * k);
             return true;
         };
         for (int q = 0; q < items && live; ++q) {
@@ -614,35 +613,72 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             uint64_t l2 = 0, l3 = 0, x2 = 0;  // sums of P, and for 1.5-entmax of sqrt(P)
             const float half = 0.5f * a.scale, t_half = -0.5f * th.t;
             const uint64_t t2 = f2pack(t_half, t_half), h2 = f2pack(half, half), c2 = f2pack(c, c);
+            uint64_t acc[32];  // fp32 output: O
+#pragma unroll
+            for (int e = 0; e < 32; ++e) acc[e] = 0;
+            auto add_o = [&]() {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float o[32];
+                    tmem_ld32(o_tm + 32 * k, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) acc[16 * k + (e >> 1)] = f2add(acc[16 * k + (e >> 1)], f2pack(o[e], o[e + 1]));
+                }
+            };
             for (int j = 0; j < nb; ++j) {
-                float v[4][32];
+                float v[kF32 ? 2 : 4][kF32 ? 16 : 32];  // fp32 output: 16 scores at a time, beside O
                 const bool diag = j == nb - 1;
-                if (!scores(v, diag)) break;
-                if (!kF32) arrive(&ctl->s_read[w]);
+                float top = -INFINITY;
+                if constexpr (kF32) {
+                    if (!wait(&ctl->s_full[w], (uint32_t)ns & 1u)) break;
+                    ++ns;
+                    tc_fence_after();
+                    if (j > 0) add_o();  // S of a block is issued after P V of the one before
+                    if (kSoftmax)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float x[32];
+                            tmem_ld32(s_tm + 32 * k, x);
+                            tmem_wait_ld(x);
+                            if (diag) hide(x, 32 * k);
+                            top = fmaxf(top, max32(x));
+                        }
+                } else {
+                    if (!scores(v, diag)) break;
+                    arrive(&ctl->s_read[w]);
+                    if (kSoftmax) top = fmaxf(fmaxf(max32(v[0]), max32(v[1])), fmaxf(max32(v[2]), max32(v[3])));
+                }
                 uint64_t off2 = 0;
                 if (kSoftmax) {
-                    const float top = fmaxf(fmaxf(max32(v[0]), max32(v[1])), fmaxf(max32(v[2]), max32(v[3])));
                     if (j == 0) {
                         m = top == -INFINITY ? 0.f : top;  // -inf: infinite inputs only (key 0 is every row's)
                     } else if (__any_sync(0xffffffffu, top > m + raise)) {
                         // O and l to the new reference, row by row (a row's numbers do not depend on its neighbours),
                         // once P V of the block before is through
-                        if (!wait(&ctl->p_empty[w], (uint32_t)(np - 1) & 1u)) break;
-                        tc_fence_after();
+                        if (!kF32) {
+                            if (!wait(&ctl->p_empty[w], (uint32_t)(np - 1) & 1u)) break;
+                            tc_fence_after();
+                        }
                         const float n = top > m + raise ? top : m, f = ex2((m - n) * c);
                         m = n;
                         const uint64_t f2 = f2pack(f, f);
                         l2 = f2mul(l2, f2);
                         l3 = f2mul(l3, f2);
+                        if constexpr (kF32) {
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            float o[32];
-                            uint32_t u[32];
-                            tmem_ld32(o_tm + 32 * k, o);
-                            tmem_wait_ld(o);
+                            for (int e = 0; e < 32; ++e) acc[e] = f2mul(acc[e], f2);
+                        } else {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
-                            tmem_st32(o_tm + 32 * k, u);
+                            for (int k = 0; k < 2; ++k) {
+                                float o[32];
+                                uint32_t u[32];
+                                tmem_ld32(o_tm + 32 * k, o);
+                                tmem_wait_ld(o);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+                                tmem_st32(o_tm + 32 * k, u);
+                            }
                         }
                     }
                     const float off = -m * c;
@@ -653,12 +689,20 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                     tc_fence_after();
                 }
                 ++np;
+                if constexpr (kF32) tmem_ld16(s_tm, v[0]);
+                constexpr int CHUNK = kF32 ? 16 : 32;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    uint32_t hi[16], mid[16], lo[16];
+                for (int k = 0; k < KB / CHUNK; ++k) {
+                    uint32_t hi[CHUNK / 2], mid[CHUNK / 2], lo[CHUNK / 2];
+                    auto& vk = v[kF32 ? k & 1 : k];
+                    if constexpr (kF32) {
+                        tmem_wait_ld16(vk);
+                        if (k + 1 < KB / CHUNK) tmem_ld16(s_tm + 16 * (k + 1), v[(k + 1) & 1]);
+                        if (diag) hide(vk, 16 * k);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const uint64_t x = f2pack(v[k][e], v[k][e + 1]);
+                    for (int e = 0; e < CHUNK; e += 2) {
+                        const uint64_t x = f2pack(vk[e], vk[e + 1]);
                         uint64_t p;
                         if (!kSoftmax) {
                             p = f2relu(f2fma(x, h2, t2));
@@ -680,10 +724,12 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         }
                     }
                     // P's columns are free once P V of the block before is through (an item's first block: its O was read)
-                    tmem_st16(p_tm + 16 * k, hi);
-                    if (kF32) {
-                        tmem_st16(p_tm + 64 + 16 * k, mid);
-                        tmem_st16(tmem + lanes + TM_P + 64u * w + 16 * k, lo);
+                    if constexpr (kF32) {
+                        tmem_st8(s_tm + 16 * k, hi);
+                        tmem_st8(s_tm + 16 * k + 8, mid);
+                        tmem_st8(p_tm + 8 * k, lo);
+                    } else {
+                        tmem_st16(p_tm + 16 * k, hi);
                     }
                 }
                 if (!live) break;
@@ -715,10 +761,16 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 ++no;
                 tc_fence_after();
                 float o[2][32];
-                tmem_ld32(o_tm, o[0]);
-                tmem_ld32(o_tm + 32, o[1]);
-                tmem_wait_ld(o[0]);
-                tmem_wait_ld(o[1]);
+                if constexpr (kF32) {
+                    add_o();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f2unpack(acc[e], o[e >> 4][2 * (e & 15)], o[e >> 4][2 * (e & 15) + 1]);
+                } else {
+                    tmem_ld32(o_tm, o[0]);
+                    tmem_ld32(o_tm + 32, o[1]);
+                    tmem_wait_ld(o[0]);
+                    tmem_wait_ld(o[1]);
+                }
                 arrive(&ctl->o_empty[w]);
                 float x0, x1;
                 f2unpack(f2add(l2, l3), x0, x1);

@@ -47,7 +47,7 @@ struct Threshold {
         const float mean = s1 * per_k, rest = (4.f - s2) * per_k + mean * mean;
         float root;
         asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(fmaxf(rest, 0.f)));
-        root = t + mean - root;
+        root = t + __fdividef((s2 - 4.f) * per_k, mean + root);  // = mean - root, which loses digits
         const bool closed = rest >= 0.f && root >= lo && pass <= CLOSED;
         const float next = closed ? root : lo;
         settled = !(fabsf(next - t) > (closed ? step : STEP_NEWTON) * s2 * per_s1);
