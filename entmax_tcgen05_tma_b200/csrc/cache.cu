@@ -602,7 +602,7 @@ int entmax_cache_compact(const entmax_cache* c, int32_t* used, void* workspace, 
 
 int entmax_cache_append(const entmax_cache* c, int layer, const void* K, long long k_stride, const void* V,
                         long long v_stride, const int32_t* seqs, const int32_t* cu, int n, int T, cudaStream_t stream) {
-    int rc = check_list(seqs, cu, n, 1 << 20);
+    int rc = check_list(seqs, cu, n, 65535);  // every warp of an entry compares its sequence with the entries before
     if (rc) return rc;
     if (!c || T < 0) return ENTMAX_ERR_ARG;
     if (layer < 0 || layer >= c->n_layers) return ENTMAX_ERR_ARG;

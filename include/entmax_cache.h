@@ -96,7 +96,8 @@ ENTMAX_API int entmax_cache_compact(const entmax_cache* c, int32_t* used, void* 
  * Tokens of T behind cu[n] are not read.  A block that holds tokens from before keeps them, moved to
  * the larger scale where the new tokens need one.  Infinite and NaN elements are stored as NaN and do not
  * count for the scale.  A page that other sequences hold too is not written (ENTMAX_ERR_ARG on the
- * device): entmax_cache_resize gives a growing sequence a page of its own.
+ * device): entmax_cache_resize gives a growing sequence a page of its own.  n <= 65535 (else
+ * ENTMAX_ERR_UNSUPPORTED).
  */
 ENTMAX_API int entmax_cache_append(const entmax_cache* c, int layer, const void* K, long long k_stride, const void* V,
                                    long long v_stride, const int32_t* seqs, const int32_t* cu, int n, int T,

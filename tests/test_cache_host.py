@@ -152,3 +152,8 @@ def test_model_pages():
     assert m.resize([0], [0]) == 0 and m.refs == [1, 0, 1, 0]
     assert m.compact() == 2 and m.table[2] == [0, 1, -1] and m.refs == [1, 1, 0, 0]
     assert m.resize([1], [192]) == 1 and m.lens == [0, 0, 66]
+
+
+@pytest.mark.parametrize("name,most", [("resize", 4096), ("fork", 65535), ("append", 65535)])
+def test_lists_have_a_longest(name, most):
+    assert call(name, cache(), n=most + 1) == E.ENTMAX_ERR_UNSUPPORTED
