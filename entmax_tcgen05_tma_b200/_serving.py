@@ -1,7 +1,8 @@
 """ctypes binding of the serving path: include/entmax_cache.h and entmax_attn_prompt.
 
 Like _binding.py: argument marshalling only.  A call works on the device of its tensors and, unless a
-stream is given, on that device's current torch stream.
+stream is given, on that device's current torch stream.  Outputs that it makes belong to that stream: as with any
+torch tensor, another stream that uses them waits for it first.
 """
 from __future__ import annotations
 
@@ -35,16 +36,19 @@ _HERE = _Here()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
 
 
-def _on(device):
-    """The device made current for the call, where it is not already."""
+def _on(device, stream=None):
+    """The device made current for the call, where it is not already, and the stream, where one is given: what the call
+    allocates belongs to the stream that it works on."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
+        return torch.cuda.stream(stream)
     return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _handle(stream, device) -> int:
     if stream is None:
         return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
-    if stream.device != device:
-        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, device))
     return int(stream.cuda_stream)
 
 
@@ -188,7 +192,7 @@ def entmax_cache_resize(cache, seqs, new_lens, short_pages=None, workspace=None,
     n = seqs.shape[0] if isinstance(seqs, torch.Tensor) and seqs.dim() == 1 else -1
     _need("seqs", seqs, (n,), torch.int32, c.device)
     _need("new_lens", new_lens, (n,), torch.int32, c.device)
-    with _on(c.device):
+    with _on(c.device, stream):
         if short_pages is None:
             short_pages = torch.empty((1,), dtype=torch.int32, device=c.device)
         else:
@@ -206,7 +210,7 @@ def entmax_cache_fork(cache, src, dst, stream=None):
     n = src.shape[0] if isinstance(src, torch.Tensor) and src.dim() == 1 else -1
     _need("src", src, (n,), torch.int32, c.device)
     _need("dst", dst, (n,), torch.int32, c.device)
-    with _on(c.device):
+    with _on(c.device, stream):
         _raise(lib.entmax_cache_fork(c._ptr, src.data_ptr(), dst.data_ptr(), n, _handle(stream, c.device)),
                "entmax_cache_fork")
 
@@ -215,7 +219,7 @@ def entmax_cache_compact(cache, used=None, workspace=None, stream=None):
     """Moves the pages in use to the front of the pool.  Returns the device tensor used (int32 [1]): the
     number of pages in use; the pages from there on are free."""
     c = _is_cache(cache)
-    with _on(c.device):
+    with _on(c.device, stream):
         if used is None:
             used = torch.empty((1,), dtype=torch.int32, device=c.device)
         else:
@@ -238,7 +242,7 @@ def entmax_cache_append(cache, layer, K, V, seqs, cu, stream=None):
     n = seqs.shape[0] if isinstance(seqs, torch.Tensor) and seqs.dim() == 1 else -1
     _need("seqs", seqs, (n,), torch.int32, c.device)
     _need("cu", cu, (n + 1,), torch.int32, c.device)
-    with _on(c.device):
+    with _on(c.device, stream):
         _raise(lib.entmax_cache_append(c._ptr, int(layer), K.data_ptr(), ks, V.data_ptr(), vs, seqs.data_ptr(),
                                        cu.data_ptr(), n, K.shape[0], _handle(stream, c.device)),
                "entmax_cache_append")
@@ -247,7 +251,7 @@ def entmax_cache_append(cache, layer, K, V, seqs, cu, stream=None):
 def entmax_cache_status(stream=None, device=None) -> int:
     """Synchronise the stream and return (and clear) the cache status word of its device."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _on(dev):
+    with _on(dev, stream):
         return int(lib.entmax_cache_status(_handle(stream, dev)))
 
 
@@ -276,7 +280,7 @@ def entmax_cache_attn(cache, layer, Q, seqs, max_len, scale=None, alpha=1.5, out
         raise ValueError("H (%d) must be a multiple of the cache's H_kv (%d)" % (H, c.H_kv))
     _need("seqs", seqs, (n,), torch.int32, c.device)
     code = _out_code(out_dtype)
-    with _on(c.device):
+    with _on(c.device, stream):
         if O is None:
             O = torch.empty((n, H, D), dtype=out_dtype, device=c.device)
         else:
@@ -312,7 +316,7 @@ def entmax_attn_prompt(Q, K, V, cu, max_len, scale=None, alpha=1.5, out_dtype=to
     n = cu.shape[0] - 1 if isinstance(cu, torch.Tensor) and cu.dim() == 1 else -1
     _need("cu", cu, (n + 1,), torch.int32, Q.device)
     code = _out_code(out_dtype)
-    with _on(Q.device):
+    with _on(Q.device, stream):
         if O is None:
             O = torch.empty((T, H, D), dtype=out_dtype, device=Q.device)
         else:

@@ -1,0 +1,153 @@
+"""The serving operators together, as a server uses them: prompts in, tokens out, beams, dropped drafts, a packed pool.
+
+Pages and blocks are compared with the plain model bit for bit after every step, attention with fp64 over what
+the cache then holds; the tolerances are those of the single operators' tests.
+"""
+import random
+
+import pytest
+import torch
+
+from cache_model import Model
+from test_gpu_cache import resize, same_pages, same_tokens
+from test_gpu_cache_attn import check as check_tokens
+from test_gpu_prompt import check as check_prompts
+from test_gpu_prompt import starts
+
+pytestmark = pytest.mark.gpu
+PAGE, LAYERS = 64, 2
+
+
+def ints(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+class Server:
+    """A cache beside its model.  A layer's projection is random: one tensor that holds Q, K and V of all new tokens."""
+
+    def __init__(self, H, H_kv, alpha, n_pages, n_seqs, max_pages, seed=0):
+        import entmax_tcgen05_tma_b200 as E
+        self.E, self.H, self.H_kv, self.alpha = E, H, H_kv, alpha
+        self.c = E.EntmaxCache.new(LAYERS, n_pages, H_kv, n_seqs, max_pages)
+        self.m = Model(LAYERS, n_pages, H_kv, n_seqs, max_pages)
+        self.g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def project(self, T):
+        x = torch.randn((T, self.H + 2 * self.H_kv, 64), generator=self.g, device="cuda").to(torch.bfloat16)
+        return x[:, :self.H], x[:, self.H:self.H + self.H_kv], x[:, self.H + self.H_kv:]
+
+    def write(self, layer, seqs, K, V, cu):
+        self.E.entmax_cache_append(self.c, layer, K, V, ints(seqs), ints(cu))
+        self.m.append(layer, K.double().cpu().numpy(), V.double().cpu().numpy(), seqs, cu)
+
+    def prompts(self, seqs, lens):
+        assert resize(self.c, self.m, seqs, lens) == 0
+        cu = starts(lens)
+        for layer in range(LAYERS):
+            Q, K, V = self.project(cu[-1])
+            out = [self.E.entmax_attn_prompt(Q, K, V, ints(cu), max(lens), alpha=self.alpha, out_dtype=t)
+                   for t in (torch.float32, torch.bfloat16)]
+            check_prompts(Q, K, V, lens, out, 0.125, self.alpha)
+            self.write(layer, seqs, K, V, cu)
+
+    def step(self, seqs):
+        """One token for each of the sequences."""
+        assert resize(self.c, self.m, seqs, [self.m.lens[s] + 1 for s in seqs]) == 0
+        for layer in range(LAYERS):
+            Q, K, V = self.project(len(seqs))
+            self.write(layer, seqs, K, V, list(range(len(seqs) + 1)))
+            O, tau = self.E.entmax_cache_attn(self.c, layer, Q, ints(seqs), PAGE * self.c.max_pages, alpha=self.alpha,
+                                              out_dtype=torch.float32)
+            check_tokens(self.c, layer, Q, seqs, O, tau, 0.125, self.alpha)
+
+    def same(self):
+        same_pages(self.c, self.m)
+        same_tokens(self.c, self.m)
+        assert self.E.entmax_cache_status() == 0
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+@pytest.mark.parametrize("H,H_kv", [(4, 4), (6, 2)])
+def test_a_server_s_day(alpha, H, H_kv):
+    s = Server(H, H_kv, alpha, n_pages=50, n_seqs=12, max_pages=8, seed=H)
+    s.prompts([0, 1, 2, 3], [1, 64, 200, 129])
+    for _ in range(3):  # sequence 1 starts a page with the first of them
+        s.step([0, 1, 2, 3])
+    # beams of sequence 2, which write tokens of their own
+    s.E.entmax_cache_fork(s.c, ints([2, 2, 2]), ints([4, 5, 6]))
+    s.m.fork([2, 2, 2], [4, 5, 6])
+    s.step([2, 4, 5, 6])
+    s.step([6, 0, 4])
+    s.same()
+    # two beams end, drafts are dropped across a page boundary, another prompt comes in beside the running ones
+    assert resize(s.c, s.m, [4, 5, 3, 1], [0, 0, 125, 60]) == 0
+    s.prompts([7, 4], [90, 33])
+    s.step([0, 1, 2, 3, 4, 6, 7])
+    s.same()
+    # the pool is packed to its front and work goes on
+    assert s.E.entmax_cache_compact(s.c).item() == s.m.compact()
+    s.same()
+    s.step([7, 6, 4, 3, 2, 1, 0])
+    s.same()
+    # a prompt that does not fit leaves everything as it is
+    assert resize(s.c, s.m, list(range(8, 12)) + [0], [512] * 4 + [500]) > 0
+    s.step([3, 0])
+    assert resize(s.c, s.m, list(range(12)), [0] * 12) == 0
+    assert s.c.refs.sum().item() == 0
+    s.same()
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_a_captured_step_replayed_over_a_page_boundary(alpha):
+    """Lengths, writes and attention of one token each as one graph, beside eager calls on the same stream."""
+    s = Server(4, 2, alpha, n_pages=30, n_seqs=6, max_pages=6, seed=3)
+    seqs, lens = [0, 1, 2], [61, 128, 7]
+    s.prompts(seqs, lens)
+    ids, cu, one = ints(seqs), ints([0, 1, 2, 3]), ints([1, 1, 1])
+    wanted = ints(lens)
+    x = torch.zeros((LAYERS, 3, 4 + 2 * 2, 64), dtype=torch.bfloat16, device="cuda")
+    O = torch.zeros((LAYERS, 3, 4, 64), device="cuda")
+    tau = torch.zeros((LAYERS, 3, 4), device="cuda")
+    short = torch.zeros(1, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        wanted.add_(one)
+        s.E.entmax_cache_resize(s.c, ids, wanted, short_pages=short)
+        for k in range(LAYERS):
+            s.E.entmax_cache_append(s.c, k, x[k, :, 4:6], x[k, :, 6:], ids, cu)
+            s.E.entmax_cache_attn(s.c, k, x[k, :, :4], ids, 6 * PAGE, alpha=alpha, out_dtype=torch.float32, O=O[k], tau=tau[k])
+    for n in range(6):  # sequence 0 passes from 61 over 64
+        x.copy_(torch.randn(x.shape, generator=s.g, device="cuda"))
+        graph.replay()
+        lens = [v + 1 for v in lens]
+        assert s.m.resize(seqs, lens) == 0 and short.item() == 0
+        for k in range(LAYERS):
+            s.m.append(k, x[k, :, 4:6].double().cpu().numpy(), x[k, :, 6:].double().cpu().numpy(), seqs, [0, 1, 2, 3])
+        s.same()
+        for k in range(LAYERS):
+            check_tokens(s.c, k, x[k, :, :4], seqs, O[k], tau[k], 0.125, alpha)
+            again = s.E.entmax_cache_attn(s.c, k, x[k, :, :4], ids, 6 * PAGE, alpha=alpha, out_dtype=torch.float32)
+            assert torch.equal(again[0], O[k]) and torch.equal(again[1], tau[k])
+        if n == 2:  # another prompt between two replays
+            s.prompts([4], [70])
+
+
+def test_calls_on_given_streams():
+    """Two streams, each with calls of its own that need workspaces of growing sizes, over one cache that no call changes."""
+    s = Server(8, 2, 1.5, n_pages=40, n_seqs=5, max_pages=10, seed=4)
+    s.prompts(list(range(5)), [300, 64, 1, 500, 129])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    rng = random.Random(0)
+    work = []
+    torch.cuda.synchronize()
+    for n in (1, 3, 5, 40, 200):
+        for stream in streams:
+            seqs = [rng.randrange(5) for _ in range(n)]
+            with torch.cuda.stream(stream):
+                Q, ids = s.project(n)[0], ints(seqs)
+            for alpha in (1.0, 1.5):
+                work.append((Q, ids, alpha, s.E.entmax_cache_attn(s.c, 1, Q, ids, 640, alpha=alpha, stream=stream)))
+    torch.cuda.synchronize()
+    for Q, ids, alpha, (O, tau) in work:
+        o, t = s.E.entmax_cache_attn(s.c, 1, Q, ids, 640, alpha=alpha)
+        assert torch.equal(O, o) and torch.equal(tau, t)
