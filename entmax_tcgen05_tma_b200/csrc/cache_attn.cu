@@ -581,8 +581,8 @@ __global__ void __launch_bounds__(JT) token_softmax_join_kernel(const TokArgs a)
 // each time it needs them.
 //
 // A page's keys go straight to registers, the next page's under way meanwhile: the fragments are whole
-// 512-byte runs of the block, there are no values to stage, and the shared memory is free for the lists of sixteen
-// warps.  (Through a ring in shared memory with eight warps this kernel took 57 us where it takes SELF.)
+// 512-byte runs of the block, there are no values to stage, and the shared memory is free for the lists of twelve
+// warps.  (Through a ring in shared memory with eight warps this kernel took 57 us of a batch call, where it takes 37.)
 constexpr int E_WARPS = 12;
 constexpr int LCAP = 28;   // entries per lane and head
 constexpr int E_KEY = 2 * LCAP * 32 * 4;                        // per warp: float [2][LCAP][32], then u16 [2][LCAP][32]

@@ -1,27 +1,34 @@
-// prompt.cu -- causal attention over packed prompts with grouped heads: entmax_attn_prompt, and its softmax
-// kernel.  (1.5-entmax and other alpha: the gather forward's PK instantiations, fwd.cu.)
+// prompt.cu -- causal attention over packed prompts with grouped heads: entmax_attn_prompt, and its kernel for
+// softmax and 1.5-entmax.  (Other alpha: the gather forward's PK instantiation, fwd.cu.)
 //
-// For row i of a sequence and its keys j <= i: S_ij = scale <Q_i, K_j>, P~ = 2^((S_ij - m_i) log2 e),
-// l_i = sum P~, O_i = (sum P~ V_j) / l_i, tau_i = m_i + ln l_i, with m_i a reference that follows the row's
-// running maximum.  Unlike the two-pass softmax forward (fwd_softmax.cu), which forms S twice and P in two
-// bf16 parts, S is formed once: m rises with the blocks, and only where it would rise by more than
-// 2^RAISE are O (in TMEM) and l brought to the new reference -- in practice in the first block or two -- so
-// the correction costs next to nothing and P~ stays below 2^RAISE.
+// Row i of a sequence and its keys j <= i: S_ij = scale <Q_i, K_j>.
+//   softmax: P_ij = 2^((S_ij - m_i) log2 e), l_i = sum P, O_i = (sum P_ij V_j) / l_i, tau_i = m_i + ln l_i, with
+//   m_i a reference that follows the row's running maximum.  S is formed once: only where m would rise by more
+//   than RAISE (a factor of 2^8) are O and l brought to the new reference, in practice in the first block or two.
+//   1.5-entmax: P_ij = ((S_ij - tau_i) / 2)^2 where positive, tau_i the root of sum P = 1; see threshold.cuh.
 //
 // A persistent CTA per SM takes pairs of 128-row tiles of one sequence and head, so that each K and V block
-// loaded serves 256 rows.  Warps 0-3 and 4-7 are the softmax of the two tiles, a thread per row (no sum or
+// loaded serves 256 rows.  Warps 0-3 and 4-7 work on the scores of the two tiles, a thread per row (no sum or
 // maximum crosses threads); warp 8 loads by TMA through a ring that runs on across the pairs; warps 9 and 10 issue
 // the products of a tile each.  S of the next block is formed as soon as this block's is in registers.
 //
-// What bounds it: one exponential a pair.  The special-function unit makes 16 a clock and SM, so 128 x 128 pairs
-// take 1024 clocks; S and P V take 256 each.  Loading S, the maxima, the waits and the rest of a warp's work
+// What bounds softmax: one exponential a score.  The special-function unit makes 16 a clock and SM, so 128 x 128
+// scores take 1024 clocks; S and P V take 256 each.  Loading S, the maxima, the waits and the rest of a warp's work
 // run beside the other tile's exponentials only in part: a pair of tiles takes about 3500 clocks where the unit alone
-// takes 2048.  Measured and not kept: a quarter or an eighth of the exponentials as polynomials on the FMA units (a
-// block's exponentials are not shortened: the polynomial's instructions take their place), two threads per row
-// (twice the waits), the two tiles' exponentials forced to alternate.
+// takes 2048.  Measured: six documents of 300 to 8192 tokens, 32 heads over 8, 290 us (650 TFLOP/s of the causal products);
+// 64 turns of 5 to 500 tokens, 12 heads, fp32 output, 60 us, where an item's latency counts (load, S, weights, P V,
+// store, one after the other).  Not kept: a quarter or an eighth of the exponentials as polynomials on the FMA units (the
+// polynomial's instructions take their place), two threads per row (twice the waits), the two tiles' exponentials
+// forced to alternate.
 //
-// P~ enters P V as one bf16 number where O is bf16 (an error of at most 2^-8 a weight, the output's own
-// rounding), and as three (24 bits) where O is fp32.
+// What bounds 1.5-entmax: the instructions of its passes over the scores, three to five of them, each about 650
+// clocks a tile's block.  Measured: ten prompts of 17 to 4096 tokens, 16 heads over 4, 187 us.  Lists of candidates, as
+// the gather forward keeps them, took 417 us on the same prompts: early rows are too dense for them.
+//
+// P enters P V as one bf16 number where O is bf16 (an error of at most 2^-8 a weight, the output's own rounding;
+// 1.5-entmax, whose supports are small, divides by the sum of the rounded weights: 2.3e-3 -> 2.05e-3 of O, 4% of the
+// time), and as three (24 bits) where O is fp32.  There a block's P V starts from zero and the blocks' are added
+// in registers: the tensor core's own additions are cut, not rounded, and grew to 7.6e-6 of O at 8192 keys (2.2e-7 so).
 #include <cuda_bf16.h>
 #include <limits.h>
 #include <math.h>
@@ -77,7 +84,8 @@ static_assert(PROMPT_SMEM <= 227 * 1024, "shared memory");
 constexpr int LOADS_AT = MAX_SEQS + 2 * (MAX_PAIRS + 2);
 static_assert(LOADS_AT % 4 == 0 && GRID % 4 == 0 && (LOADS_AT + (1 + BALANCED) * GRID + LIST) * 4 <= NS * 2 * BLOCK16, "list scratch");
 // TMEM columns: S of tile w at 128 w, O at 256 + 64 w, P at 384 + 64 w, so that S of the next block is formed while
-// this block's P is.  Three parts do not fit beside S: the first two then lie over S, and the third at P's place.
+// this block's P is.  Three parts do not fit beside S: each 16 scores' first two then lie in their place, 8 columns
+// each, and the third at P's place.
 constexpr int TM_S = 0, TM_O = 256, TM_P = 384;
 
 // Blocks of tile w of a pair: its last block holds the diagonal.
@@ -114,6 +122,15 @@ __device__ __forceinline__ float above0(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+// sum[0] and sum[1] plus the two numbers of a bf16 pair.
+__device__ __forceinline__ void add_bf16(float (&sum)[2], uint32_t pair) {
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "add.rn.f32.bf16 %0, lo, %0;\n\t"
+        "add.rn.f32.bf16 %1, hi, %1;\n\t}"
+        : "+f"(sum[0]), "+f"(sum[1])
+        : "r"(pair));
 }
 
 // Two fp32 values as three bf16 pairs: the top 16 bits, the top 16 bits of the rest, and its rest rounded.
@@ -594,7 +611,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         f2unpack(k2, kx, ky);
                         f2unpack(f2add(s1, s3), x0, x1);
                         f2unpack(f2add(s2, s4), y0, y1);
-                        th.step(count ? kx + ky : -1.f, x0 + x1, y0 + y1, pass, kF32 ? 5e-3f : 0.02f);
+                        th.step(count ? kx + ky : -1.f, x0 + x1, y0 + y1, pass, kF32 ? 3e-3f : 0.02f);
                     }
                     const bool any = __any_sync(0xffffffffu, !th.settled && pass < MOST_PASSES);
                     if (lane == 0) {
@@ -611,6 +628,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             // at the threshold found
             float m = -INFINITY;
             uint64_t l2 = 0, l3 = 0, x2 = 0;  // sums of P, and for 1.5-entmax of sqrt(P)
+            float rounded[2] = {0.f, 0.f};  // of P as it enters P V
             const float half = 0.5f * a.scale, t_half = -0.5f * th.t;
             const uint64_t t2 = f2pack(t_half, t_half), h2 = f2pack(half, half), c2 = f2pack(c, c);
             uint64_t acc[32];  // fp32 output: O
@@ -721,6 +739,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                             float x0, x1;
                             f2unpack(p, x0, x1);
                             hi[e >> 1] = pack_bf16(x0, x1);
+                            if (!kSoftmax) add_bf16(rounded, hi[e >> 1]);
                         }
                     }
                     // P's columns are free once P V of the block before is through (an item's first block: its O was read)
@@ -782,6 +801,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                 } else if (!odd) {  // a last Newton step on sum P = 1: what is left of tau's error squared
                     f2unpack(x2, x0, x1);
                     tau = th.t + (l - 1.f) / (x0 + x1);
+                    if (!kF32) {
+                        inv = 1.f / (rounded[0] + rounded[1]);
+                    }
                 }
                 if (i < it.len) {
                     const size_t t = (size_t)(it.first + i);

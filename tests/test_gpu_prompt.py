@@ -3,7 +3,7 @@
 Tolerances.  Scores are sums of 64 exact products in fp32, scaled once: |dS| <= delta = 2^-18 (1 + max|S|).
   softmax, fp32 output:  a weight has the relative error 2 delta + 2^-20 (exp2, sums; three bf16 parts: 2^-24), so
                |dO| <= (2 delta + 2^-20) sum p |V|.
-  softmax, bf16 output:  2 delta + 2^-8 (one bf16 part, half a step) + 2^-18 (exponentials from a polynomial: 2.8e-6),
+  softmax, bf16 output:  2 delta + 2^-8 (one bf16 part, half a step) + 2^-18 (exponentials and sums),
                then the output's own rounding, 2^-8 |O|.   |dtau| <= delta + 2^-18 (1 + |tau|) for both.
   1.5-entmax:  tau moves by at most delta, plus what the solver leaves: 1.3e-5 of the support's mean depth (at most 2)
                and 2^-22 of the scores' size; with e the sum of both and of delta, |dp| <= e (sqrt p + e) for the keys
@@ -309,3 +309,51 @@ def test_refusals():
         E.entmax_attn_prompt(Q, K, V, cu.long(), 100)
     O, tau = E.entmax_attn_prompt(Q[:0], K[:0], V[:0], ints([0]), 0)
     assert O.shape == (0, 4, 64) and tau.shape == (4, 0)
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_fp32_outputs_of_long_rows(alpha):
+    """The error of an fp32 output does not grow with the keys: at most 2^-20 of the rows' size.  A score of up to 64
+    products is off by a few 2^-24 of its size (below 8 here), so a weight by less than 2^-20 and independently of the next;
+    P enters with 24 bits, P V of 128 keys is added in the tensor core and the blocks' sums in fp32, rounded."""
+    from entmax_tcgen05_tma_b200 import entmax_attn_prompt
+    L = 6000
+    Q, K, V = inputs(L, 1, 1, seed=12)
+    O, _ = entmax_attn_prompt(Q, K, V, ints([0, L]), L, alpha=alpha, out_dtype=torch.float32)
+    P = 0.125 * (Q[:, 0].double() @ K[:, 0].double().T)
+    P.masked_fill_(torch.ones(L, L, dtype=torch.bool, device="cuda").triu_(1), float("-inf"))
+    if alpha == 1.0:
+        P = P.softmax(-1)
+    else:  # Newton's method on sum max(0, S - t)^2 = 4 from below: convex and decreasing, so t rises to the root
+        t = P.amax(-1, keepdim=True) - 2
+        for _ in range(30):
+            d = (P - t).clamp_(min=0)
+            t += (d.square().sum(-1, keepdim=True) - 4) / (2 * d.sum(-1, keepdim=True))
+        P = ((P - t) / 2).clamp_(min=0).square_()
+    ref = P @ V[:, 0].double()
+    err = (O[:, 0].double() - ref).norm(dim=-1) / ref.norm(dim=-1)
+    assert err.square().mean().sqrt().item() <= 2.0 ** -20
+    tail = err[-1000:].square().mean().sqrt().item()
+    assert tail <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_more_items_than_a_launch_lists(alpha):
+    """4096 prompts of one to three tokens under 48 heads: 196608 work items, where a launch of 148 blocks takes 151552.  A first
+    row's weight is 1: its output is V, and tau is the score (softmax) or the score less 2."""
+    from entmax_tcgen05_tma_b200 import entmax_attn_prompt
+    lens = [1 + (i * 7) % 3 for i in range(4096)]
+    cu = starts(lens)
+    Q, K, V = inputs(cu[-1], 48, 4, seed=13)
+    O, tau = entmax_attn_prompt(Q, K, V, ints(cu), 3, alpha=alpha, out_dtype=torch.float32)
+    assert torch.isfinite(O).all() and torch.isfinite(tau).all()
+    first = torch.tensor(cu[:-1], device="cuda")
+    k, v = (x[first].double().repeat_interleave(12, 1) for x in (K, V))
+    S = 0.125 * (Q[first].double() * k).sum(-1)
+    delta = 2.0 ** -18 * (1 + S.abs().max().item())
+    assert (tau[:, first].T.double() - (S if alpha == 1.0 else S - 2)).abs().max().item() <= delta + 2.0 ** -18 * 8
+    assert (O[first].double() - v).abs().max().item() <= (2 * delta + 2.0 ** -20) * v.abs().max().item()
+    # the last sequence in full
+    n, a = lens[-1], cu[-2]
+    ref = reference(Q[a:], K[a:], V[a:], [n], 0.125, alpha)[0]
+    assert np.abs(O[a:].double().cpu().numpy() - ref).max() <= 1e-4
