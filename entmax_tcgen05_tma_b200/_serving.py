@@ -109,7 +109,7 @@ class EntmaxCache:
     """
 
     __slots__ = ("K", "V", "k_scale", "v_scale", "refs", "table", "lens", "n_layers", "n_pages", "H_kv", "n_seqs",
-                 "max_pages", "device", "_struct", "_ptr", "_ws_bytes", "_ws")
+                 "max_pages", "device", "_struct", "_ptr", "_ws_bytes", "_attn_ws", "_ws")
 
     def __init__(self, K, V, k_scale, v_scale, refs, table, lens):
         if not isinstance(K, torch.Tensor) or K.dim() != 5:
@@ -135,6 +135,7 @@ class EntmaxCache:
                                     refs.data_ptr(), table.data_ptr(), lens.data_ptr(), nl, npg, hk, ns, mp)
         self._ptr = ctypes.addressof(self._struct)
         self._ws_bytes = int(lib.entmax_cache_workspace_size(self._ptr))
+        self._attn_ws = {}  # (n, H, alpha) -> bytes
         self._ws = {}  # stream handle -> workspace: calls on one stream follow each other
 
     @classmethod
@@ -194,7 +195,7 @@ def entmax_cache_resize(cache, seqs, new_lens, short_pages=None, workspace=None,
     _need("new_lens", new_lens, (n,), torch.int32, c.device)
     with _on(c.device, stream):
         if short_pages is None:
-            short_pages = torch.empty((1,), dtype=torch.int32, device=c.device)
+            short_pages = torch.empty(1, dtype=torch.int32, device=c.device)
         else:
             _need("short_pages", short_pages, (1,), torch.int32, c.device)
         h = _handle(stream, c.device)
@@ -221,7 +222,7 @@ def entmax_cache_compact(cache, used=None, workspace=None, stream=None):
     c = _is_cache(cache)
     with _on(c.device, stream):
         if used is None:
-            used = torch.empty((1,), dtype=torch.int32, device=c.device)
+            used = torch.empty(1, dtype=torch.int32, device=c.device)
         else:
             _need("used", used, (1,), torch.int32, c.device)
         h = _handle(stream, c.device)
@@ -282,15 +283,18 @@ def entmax_cache_attn(cache, layer, Q, seqs, max_len, scale=None, alpha=1.5, out
     code = _out_code(out_dtype)
     with _on(c.device, stream):
         if O is None:
-            O = torch.empty((n, H, D), dtype=out_dtype, device=c.device)
+            O = torch.empty(n, H, D, dtype=out_dtype, device=c.device)
         else:
             _need("O", O, (n, H, D), out_dtype, c.device)
         if tau is None:
-            tau = torch.empty((n, H), dtype=torch.float32, device=c.device)
+            tau = torch.empty(n, H, dtype=torch.float32, device=c.device)
         else:
             _need("tau", tau, (n, H), torch.float32, c.device)
         h = _handle(stream, c.device)
-        ws, ws_bytes = _workspace(c, workspace, lib.entmax_cache_attn_workspace_size(n, H, c.H_kv, alpha), h)
+        need = c._attn_ws.get((n, H, alpha))
+        if need is None:
+            need = c._attn_ws[n, H, alpha] = lib.entmax_cache_attn_workspace_size(n, H, c.H_kv, alpha)
+        ws, ws_bytes = _workspace(c, workspace, need, h)
         _raise(lib.entmax_cache_attn(c._ptr, layer, Q.data_ptr(), qs, seqs.data_ptr(), n, max_len,
                                      D ** -0.5 if scale is None else scale, alpha, H, O.data_ptr(), code,
                                      tau.data_ptr(), ws, ws_bytes, h), "entmax_cache_attn")
@@ -318,11 +322,11 @@ def entmax_attn_prompt(Q, K, V, cu, max_len, scale=None, alpha=1.5, out_dtype=to
     code = _out_code(out_dtype)
     with _on(Q.device, stream):
         if O is None:
-            O = torch.empty((T, H, D), dtype=out_dtype, device=Q.device)
+            O = torch.empty(T, H, D, dtype=out_dtype, device=Q.device)
         else:
             _need("O", O, (T, H, D), out_dtype, Q.device)
         if tau is None:
-            tau = torch.empty((H, T), dtype=torch.float32, device=Q.device)
+            tau = torch.empty(H, T, dtype=torch.float32, device=Q.device)
         else:
             _need("tau", tau, (H, T), torch.float32, Q.device)
         _raise(lib.entmax_attn_prompt(Q.data_ptr(), qs, K.data_ptr(), ks, V.data_ptr(), vs, cu.data_ptr(), n, T,

@@ -15,14 +15,14 @@
 // What bounds softmax: one exponential a score.  The special-function unit makes 16 a clock and SM, so 128 x 128
 // scores take 1024 clocks; S and P V take 256 each.  Loading S, the maxima, the waits and the rest of a warp's work
 // run beside the other tile's exponentials only in part: a pair of tiles takes about 3500 clocks where the unit alone
-// takes 2048.  Measured: six documents of 300 to 8192 tokens, 32 heads over 8, 290 us (650 TFLOP/s of the causal products);
-// 64 turns of 5 to 500 tokens, 12 heads, fp32 output, 60 us, where an item's latency counts (load, S, weights, P V,
-// store, one after the other).  Not kept: a quarter or an eighth of the exponentials as polynomials on the FMA units (the
+// takes 2048.  Measured: three documents of 8192, 4097 and 2999 tokens, 16 heads over 4, 290 us (656 TFLOP/s of the causal
+// products); 32 turns of 64 to 512 tokens, 12 heads, fp32 output, 60 us, where an item's latency counts (load, S, weights,
+// P V, store, one after the other).  Not kept: a quarter or an eighth of the exponentials as polynomials on the FMA units (the
 // polynomial's instructions take their place), two threads per row (twice the waits), the two tiles' exponentials
 // forced to alternate.
 //
 // What bounds 1.5-entmax: the instructions of its passes over the scores, three to five of them, each about 650
-// clocks a tile's block.  Measured: ten prompts of 17 to 4096 tokens, 16 heads over 4, 187 us.  Lists of candidates, as
+// clocks a tile's block.  Measured: six prompts of 1 to 4096 tokens, 12 heads, 187 us.  Lists of candidates, as
 // the gather forward keeps them, took 417 us on the same prompts: early rows are too dense for them.
 //
 // P enters P V as one bf16 number where O is bf16 (an error of at most 2^-8 a weight, the output's own rounding;

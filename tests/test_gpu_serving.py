@@ -151,3 +151,61 @@ def test_calls_on_given_streams():
     for Q, ids, alpha, (O, tau) in work:
         o, t = s.E.entmax_cache_attn(s.c, 1, Q, ids, 640, alpha=alpha)
         assert torch.equal(O, o) and torch.equal(tau, t)
+
+
+@pytest.mark.parametrize("what", ["prompt", "resize", "append", "softmax", "entmax", "fork", "compact"])
+def test_first_call_of_a_host_thread(what):
+    """A new thread's first CUDA work is the call itself (all of its tensors exist): the results are the main thread's."""
+    import threading
+    s = Server(4, 2, 1.5, n_pages=20, n_seqs=4, max_pages=4, seed=6)
+    s.prompts([0, 1], [100, 33])
+    E, c = s.E, s.c
+    Q, K, V = s.project(7)
+    cu, ids, ends, short = ints([0, 4, 7]), ints([0, 1]), ints([104, 36]), ints([0])
+    O, tau = torch.zeros(7, 4, 64, device="cuda"), torch.zeros(4, 7, device="cuda")
+    o, t = torch.zeros(2, 4, 64, device="cuda"), torch.zeros(2, 4, device="cuda")
+    src, dst = ints([0]), ints([3])
+    ws = torch.zeros(max(E.entmax_cache_workspace_size(c), E.entmax_cache_attn_workspace_size(2, 4, 2, 1.0),
+                         E.entmax_cache_attn_workspace_size(2, 4, 2, 1.5)), dtype=torch.uint8, device="cuda")
+    f32 = torch.float32
+    calls = {
+        "prompt": lambda: E.entmax_attn_prompt(Q, K, V, cu, 4, out_dtype=f32, O=O, tau=tau),
+        "resize": lambda: E.entmax_cache_resize(c, ids, ends, short, workspace=ws),
+        "append": lambda: E.entmax_cache_append(c, 1, K[:2], V[:2], ids, ints_cu),
+        "softmax": lambda: E.entmax_cache_attn(c, 1, Q[:2], ids, 256, alpha=1.0, out_dtype=f32, O=o, tau=t, workspace=ws),
+        "entmax": lambda: E.entmax_cache_attn(c, 1, Q[:2], ids, 256, out_dtype=f32, O=o, tau=t, workspace=ws),
+        "fork": lambda: E.entmax_cache_fork(c, src, dst),
+        "compact": lambda: E.entmax_cache_compact(c, short, workspace=ws),
+    }
+    ints_cu = ints([0, 1, 2])
+    torch.cuda.synchronize()
+    errors = []
+
+    def work():
+        try:
+            calls[what]()
+        except Exception as e:  # reported below, on the main thread
+            errors.append(e)
+
+    th = threading.Thread(target=work)
+    th.start()
+    th.join(60)
+    torch.cuda.synchronize()
+    assert not errors, errors
+    assert E.entmax_cache_status() == 0
+    if what == "prompt":
+        a = E.entmax_attn_prompt(Q, K, V, cu, 4, out_dtype=f32)
+        assert torch.equal(a[0], O) and torch.equal(a[1], tau)
+    elif what in ("softmax", "entmax"):
+        a = E.entmax_cache_attn(c, 1, Q[:2], ids, 256, alpha=1.0 if what == "softmax" else 1.5, out_dtype=f32)
+        assert torch.equal(a[0], o) and torch.equal(a[1], t)
+    else:
+        if what == "resize":
+            assert s.m.resize([0, 1], [104, 36]) == short.item() == 0
+        elif what == "append":
+            s.m.append(1, K[:2].double().cpu().numpy(), V[:2].double().cpu().numpy(), [0, 1], [0, 1, 2])
+        elif what == "fork":
+            s.m.fork([0], [3])
+        else:
+            assert s.m.compact() == short.item()
+        s.same()
