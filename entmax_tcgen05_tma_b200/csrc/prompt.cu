@@ -23,7 +23,7 @@
 //
 // What bounds 1.5-entmax: the instructions of its passes over the scores, three to five of them, each about 650
 // clocks a tile's block.  Measured: six prompts of 1 to 4096 tokens, 12 heads, 187 us.  Lists of candidates, as
-// the gather forward keeps them, took 417 us on the same prompts: early rows are too dense for them.
+// the gather forward keeps them, took 2051 us on the same prompts: early rows are too dense for them.
 //
 // P enters P V as one bf16 number where O is bf16 (an error of at most 2^-8 a weight, the output's own rounding;
 // 1.5-entmax, whose supports are small, divides by the sum of the rounded weights: 2.3e-3 -> 2.05e-3 of O, 4% of the
