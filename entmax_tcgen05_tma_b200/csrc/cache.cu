@@ -384,14 +384,15 @@ constexpr int PAGE_ADD = 2 * (PAGE - 1);
 // One warp per (page, K or V, head) block.  A new token's row of a head is 128 bytes in and 64 bytes out: 8
 // lanes read and write a row, 16 bytes and 8 bytes each, so a warp moves four rows per step and holds a
 // whole block's new rows in registers between the largest-value pass and the conversion.  Bound by HBM
-// for prompts (2 bytes read, 1 written per number: 116 MB in 25 us, 70% of the copy rate) and by the chain of index
-// loads for single tokens (5 us for 64 sequences).
-__global__ void __launch_bounds__(256) append_kernel(const CacheArgs c, int layer, const uint16_t* __restrict__ K,
-                                                     long long k_stride, const uint16_t* __restrict__ V,
-                                                     long long v_stride, const int* __restrict__ seqs,
-                                                     const int* __restrict__ cu, int n, int T, long long items) {
+// for prompts (2 bytes read, 1 written per number: 116 MB in 22 us, 80% of the copy rate) and by the chain of index
+// loads for single tokens (5 us for 64 sequences).  80 registers a thread, so that six CTAs fit an SM: with the 114 that
+// hold everything without spilling, four do and it takes 24 us.
+__global__ void __launch_bounds__(128, 6) append_kernel(const CacheArgs c, int layer, const uint16_t* __restrict__ K,
+                                                        long long k_stride, const uint16_t* __restrict__ V,
+                                                        long long v_stride, const int* __restrict__ seqs,
+                                                        const int* __restrict__ cu, int n, int T, long long items) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * 8 + warp;
+    const long long w = (long long)blockIdx.x * 4 + warp;
     const int per = 2 * c.Hkv;
     const long long item = w / per;
     if (item >= items) return;
@@ -401,32 +402,19 @@ __global__ void __launch_bounds__(256) append_kernel(const CacheArgs c, int laye
     const long long k = item - unit_base(c0, i, PAGE, PAGE_ADD);
     if (c0 == c1 || k < 0) return;
     bool bad = c0 < 0 || c1 < c0 || c1 > T || s < 0 || s >= c.n_seqs;
-    if (!bad) {
+    const int len = bad ? 0 : c.lens[s], start = len - (c1 - c0);
+    if (!bad)
         for (int j = lane; j < i; j += 32) bad |= seqs[j] == s;
-        bad = __any_sync(0xffffffffu, bad);
-    }
-    int len = 0, start = 0, page = 0;
-    long long pg = 0;
-    if (!bad) {
-        len = c.lens[s];
-        start = len - (c1 - c0);
-        bad = start < 0 || len > c.max_pages * PAGE;
-    }
-    if (!bad) {
-        pg = start / PAGE + k;
-        if (pg * PAGE >= len) return;
-        page = c.table[(size_t)s * c.max_pages + pg];
-        bad = page < 0 || page >= c.n_pages || c.refs[page] != 1;
-    }
-    if (bad) {
+    bad |= start < 0 || len > c.max_pages * PAGE;
+    if (__any_sync(0xffffffffu, bad)) {
         if (lane == 0) cache_error(c);
         return;
     }
+    const long long pg = start / PAGE + k;
+    if (pg * PAGE >= len) return;
+    const int page = c.table[(size_t)s * c.max_pages + pg];
     const int p0 = (int)pg * PAGE;
     const int a = max(start - p0, 0), b = min(len - p0, PAGE);  // rows a .. b - 1 are new, rows before a stay
-    const size_t blk = c.block(layer, page, head);
-    uint8_t* rows = (is_v ? c.V : c.K) + blk * BLOCK_BYTES;
-    float* scale = (is_v ? c.vs : c.ks) + blk;
     const long long stride = is_v ? v_stride : k_stride;
     const uint16_t* in = (is_v ? V : K) + (long long)(c0 + p0 - start) * stride + head * 64;  // row r at r * stride, r >= a
 
@@ -438,6 +426,14 @@ __global__ void __launch_bounds__(256) append_kernel(const CacheArgs c, int laye
         x[j] = make_uint4(0, 0, 0, 0);
         if (r >= a && r < b) x[j] = __ldg(reinterpret_cast<const uint4*>(in + (long long)r * stride) + ch);
     }
+    // the new rows are under way while the page is looked up
+    if (page < 0 || page >= c.n_pages || c.refs[page] != 1) {
+        if (lane == 0) cache_error(c);
+        return;
+    }
+    const size_t blk = c.block(layer, page, head);
+    uint8_t* rows = (is_v ? c.V : c.K) + blk * BLOCK_BYTES;
+    float* scale = (is_v ? c.vs : c.ks) + blk;
     const float old = a > 0 ? *scale : 0.f;
     // largest magnitude as bf16 bits (their order is that of the magnitudes); infinities and NaN become NaN
     // and do not count
@@ -615,8 +611,8 @@ int entmax_cache_append(const entmax_cache* c, int layer, const void* K, long lo
     rc = cache_args(c, &a);
     if (rc || n == 0 || T == 0) return rc;
     const long long items = unit_base(T, n, PAGE, PAGE_ADD) + 1, warps = items * 2 * c->H_kv;
-    if ((warps + 7) / 8 > 0x7fffffffll) return ENTMAX_ERR_UNSUPPORTED;
-    append_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(a, layer, static_cast<const uint16_t*>(K), k_stride,
+    if ((warps + 3) / 4 > 0x7fffffffll) return ENTMAX_ERR_UNSUPPORTED;
+    append_kernel<<<(unsigned)((warps + 3) / 4), 128, 0, stream>>>(a, layer, static_cast<const uint16_t*>(K), k_stride,
                                                                   static_cast<const uint16_t*>(V), v_stride, seqs, cu,
                                                                   n, T, items);
     return abi_record(cudaGetLastError());
