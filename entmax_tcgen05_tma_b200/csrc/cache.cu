@@ -6,6 +6,7 @@
 // are taken lowest number first in the order of the caller's list, and atomics only add, subtract or
 // take extremes of integers.
 #include <cuda_bf16.h>
+#include <algorithm>
 #include <mutex>
 #include "cache.cuh"
 #include "common.cuh"
@@ -259,9 +260,10 @@ __global__ void __launch_bounds__(PT) resize_kernel(const CacheArgs c, const int
 
 // ---------------------------------------------------------------------------------------- copies
 // Copies pages src[j] -> dst[j], j < *count, all layers: for each layer and of K and V a page is
-// H_kv * 4 KB in one piece.  Bound by HBM: 16 KB pieces, 64 bytes in flight per thread; 951 MB read and
-// written in 175 us, 83% of the copy rate.  kRenumber: the
-// pages moved, so table entries that name map[p] >= 0 follow (compact).
+// H_kv * 4 KB in one piece.  Bound by HBM: 32 KB pieces, 128 bytes in flight per thread; 951 MB read and
+// written in 143 us, the copy rate.  kRenumber: the pages moved, so table entries that name map[p] >= 0
+// follow (compact).
+constexpr int COPY_PIECE = 32768;
 template <bool kRenumber>
 __global__ void __launch_bounds__(256) copy_pages_kernel(const CacheArgs c, const int* src, const int* dst, const int* count,
                                                          const int* map) {
@@ -277,7 +279,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const CacheArgs c, cons
             }
         }
     }
-    const size_t piece = 16384, bytes = (size_t)c.Hkv * BLOCK_BYTES;
+    const size_t piece = COPY_PIECE, bytes = (size_t)c.Hkv * BLOCK_BYTES;
     const size_t per = (bytes + piece - 1) / piece;  // pieces of a page's layer
     const size_t total = (size_t)n * c.n_layers * 2 * per;
     for (size_t u = blockIdx.x; u < total; u += gridDim.x) {
@@ -291,12 +293,12 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const CacheArgs c, cons
         const uint4* a = reinterpret_cast<const uint4*>(pool + from * BLOCK_BYTES + q * piece);
         uint4* b = reinterpret_cast<uint4*>(pool + to * BLOCK_BYTES + q * piece);
         const int m = (int)(min(piece, bytes - q * piece) / 16);
-        uint4 x[4];
+        uint4 x[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (threadIdx.x + 256 * k < m) x[k] = __ldcs(a + threadIdx.x + 256 * k);
+        for (int k = 0; k < 8; ++k)
+            if (threadIdx.x + 256 * k < m) x[k] = __ldg(a + threadIdx.x + 256 * k);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
             if (threadIdx.x + 256 * k < m) b[threadIdx.x + 256 * k] = x[k];
         if (q == 0) {
             float* sc = t ? c.vs : c.ks;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const CacheArgs c, cons
 }
 
 // ---------------------------------------------------------------------------------------- compact
-// One CTA (5 us for 2500 pages, beside copies of 175): counts the pages in use, then pairs the used pages at or above that count with the free pages
+// One CTA (5 us for 2500 pages, beside copies of 143): counts the pages in use, then pairs the used pages at or above that count with the free pages
 // below it, both in order.  ws.a, ws.b: the pairs; ws.c: the page's new number or -1.
 __global__ void __launch_bounds__(PT) compact_plan_kernel(const CacheArgs c, int* used_out, const PageWs ws) {
     __shared__ int part[32];
@@ -533,7 +535,12 @@ int cache_args(const entmax_cache* c, CacheArgs* out) {
 using namespace entmax;
 
 namespace {
-constexpr int COPY_GRID = 148 * 8;
+// CTAs for copies of at most `pages` pages.  Up to 64 an SM although 8 are resident: pieces dealt out by the hardware
+// as CTAs end take 143 us where 8 CTAs an SM that each loop over their share take 171 (951 MB).
+int copy_grid(const entmax_cache* c, long long pages) {
+    const long long most = pages * c->n_layers * 2 * ((c->H_kv * (long long)BLOCK_BYTES + COPY_PIECE - 1) / COPY_PIECE);
+    return (int)std::min(std::max(most, 1ll), 148ll * 64);
+}
 // The cache's host-side checks without the look-up of the device status word (no CUDA call).
 int check_list(const void* a, const void* b, int n, int most) {
     if (n < 0) return ENTMAX_ERR_ARG;
@@ -571,7 +578,7 @@ int entmax_cache_resize(const entmax_cache* c, const int32_t* seqs, const int32_
     resize_kernel<<<1, PT, smem, stream>>>(a, seqs, new_lens, n, short_pages, ws);
     rc = abi_record(cudaGetLastError());
     if (rc || n == 0) return rc;
-    return abi_record(launch_next(copy_pages_kernel<false>, COPY_GRID, 256, stream, a, ws.pairs, ws.pairs + MAX_LIST, ws.count, nullptr));
+    return abi_record(launch_next(copy_pages_kernel<false>, copy_grid(c, n), 256, stream, a, ws.pairs, ws.pairs + MAX_LIST, ws.count, nullptr));
 }
 
 int entmax_cache_fork(const entmax_cache* c, const int32_t* src, const int32_t* dst, int n, cudaStream_t stream) {
@@ -595,7 +602,7 @@ int entmax_cache_compact(const entmax_cache* c, int32_t* used, void* workspace, 
     compact_plan_kernel<<<1, PT, 0, stream>>>(a, used, ws);
     rc = abi_record(cudaGetLastError());
     if (rc) return rc;
-    return abi_record(launch_next(copy_pages_kernel<true>, COPY_GRID, 256, stream, a, ws.a, ws.b, ws.count, ws.c));
+    return abi_record(launch_next(copy_pages_kernel<true>, std::max(148, copy_grid(c, c->n_pages / 2)), 256, stream, a, ws.a, ws.b, ws.count, ws.c));
 }
 
 int entmax_cache_append(const entmax_cache* c, int layer, const void* K, long long k_stride, const void* V,
