@@ -439,6 +439,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
                         if (ok && j < nb) ok = wait(&ctl->k_full[st], (uint32_t)((n_kv + j) / NS) & 1u);
                         auto form_s = [&]() {
                             ok = ok && wait(&ctl->s_read[w], ((uint32_t)ns & 1u) ^ 1u);  // the block before is in registers
+                            // fp32 output: and P V, which reads P where S comes to lie (products of different shapes have
+                            // no order of their own)
+                            if (kF32 && np > 0) ok = ok && wait(&ctl->p_empty[w], (uint32_t)(np - 1) & 1u);
                             if (!ok) return;
                             tc_fence_after();
                             const uint64_t dq = umma_desc_kmajor_sw128(q_u + qb * 2 * TILE_BYTES);
