@@ -357,3 +357,49 @@ def test_more_items_than_a_launch_lists(alpha):
     n, a = lens[-1], cu[-2]
     ref = reference(Q[a:], K[a:], V[a:], [n], 0.125, alpha)[0]
     assert np.abs(O[a:].double().cpu().numpy() - ref).max() <= 1e-4
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5, 1.25])
+def test_offsets_past_32_bits(alpha):
+    """Tokens 2.3e9 elements into a fused projection and an output: the bits of the same tokens alone."""
+    from entmax_tcgen05_tma_b200 import entmax_attn_prompt
+    T, lens, H, H_kv = 900000, [200, 300], 38, 1
+    Q, K, V = inputs(500, H, H_kv, 16)
+    x = torch.empty((T, H + 2 * H_kv, 64), dtype=torch.bfloat16, device="cuda")
+    x[-501:-500] = float("nan")
+    x[-500:] = torch.cat((Q, K, V), 1)
+    O = torch.empty((T, H, 64), dtype=torch.bfloat16, device="cuda")
+    O[-501] = 7.0
+    o, tau = entmax_attn_prompt(x[:, :H], x[:, H:H + 1], x[:, H + 1:], ints([T - 500, T - 300, T]), 300, alpha=alpha, O=O)
+    a, t = entmax_attn_prompt(Q, K, V, ints([0, 200, 500]), 300, alpha=alpha)
+    assert torch.equal(o[-500:], a) and torch.equal(tau[:, -500:], t)
+    assert (O[-501] == 7.0).all()
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_a_very_long_sequence(alpha):
+    """131072 tokens beside one, and the largest max_len: the last rows against fp64."""
+    from entmax_tcgen05_tma_b200 import entmax_attn_prompt
+    L = 131072
+    Q, K, V = inputs(L + 1, 1, 1, 17)
+    O, tau = entmax_attn_prompt(Q, K, V, ints([0, L, L + 1]), 1 << 20, alpha=alpha, out_dtype=torch.float32)
+    rows = torch.tensor([0, 1, 127, 128, 4095, 70001, L - 2, L - 1], device="cuda")
+    S = 0.125 * (Q[rows, 0].double() @ K[:L, 0].double().T)
+    S.masked_fill_(torch.arange(L, device="cuda")[None] > rows[:, None], float("-inf"))
+    delta = 2.0 ** -18 * (1 + torch.where(S.isinf(), 0.0, S).abs().max().item())
+    if alpha == 1.0:
+        t = S.logsumexp(-1)
+        P = (S - t[:, None]).exp()
+        room = (2 * delta + 2.0 ** -20) * (P @ V[:L, 0].double().abs())
+    else:  # Newton's method from below, as above
+        t = S.amax(-1) - 2
+        for _ in range(40):
+            d = (S - t[:, None]).clamp_(min=0)
+            t += (d.square().sum(-1) - 4) / (2 * d.sum(-1))
+        w = ((S - t[:, None]) / 2).clamp_(min=0)
+        P = w.square()
+        e = 2 * delta + 2.6e-5 + 2.0 ** -22 * (1 + t.abs().max().item())
+        room = (e * (w + e) * (S > t[:, None] - 2 * e) + 2.0 ** -20 * P) @ V[:L, 0].double().abs()
+    assert ((O[rows, 0].double() - P @ V[:L, 0].double()).abs() <= room).all()
+    assert (tau[0, rows].double() - t).abs().max().item() <= delta + 2.6e-5 + 2.0 ** -18 * (1 + t.abs().max().item())
+    assert torch.equal(O[L, 0], V[L, 0].float())
