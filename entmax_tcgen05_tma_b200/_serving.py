@@ -7,6 +7,7 @@ torch tensor, another stream that uses them waits for it first.
 from __future__ import annotations
 
 import ctypes
+from threading import get_ident
 
 import torch
 
@@ -136,7 +137,7 @@ class EntmaxCache:
         self._ptr = ctypes.addressof(self._struct)
         self._ws_bytes = int(lib.entmax_cache_workspace_size(self._ptr))
         self._attn_ws = {}  # (n, H, alpha) -> bytes
-        self._ws = {}  # stream handle -> workspace: calls on one stream follow each other
+        self._ws = {}  # (stream handle, thread) -> workspace
 
     @classmethod
     def new(cls, n_layers: int, n_pages: int, H_kv: int, n_seqs: int, max_pages: int, device="cuda"):
@@ -158,8 +159,9 @@ def _is_cache(cache):
 
 
 def _workspace(cache, given, nbytes, handle):
-    """The caller's workspace, or the cache's own for the stream (kept, and grown where needed).  A call that is being
-    captured gets a buffer of its graph's: graphs captured on one stream may be replayed side by side."""
+    """The caller's workspace, or the cache's own for the stream and host thread (kept, and grown where needed): the
+    launches of one call follow each other on the stream, but another thread's may come between them.  A call that is
+    being captured gets a buffer of its graph's: graphs captured on one stream may be replayed side by side."""
     if given is not None:
         if not isinstance(given, torch.Tensor) or given.device != cache.device \
                 or given.numel() * given.element_size() < nbytes:
@@ -168,10 +170,11 @@ def _workspace(cache, given, nbytes, handle):
     if torch.cuda.is_current_stream_capturing():
         ws = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=cache.device)
         return ws.data_ptr(), nbytes
-    kept = cache._ws.get(handle)
+    key = handle, get_ident()
+    kept = cache._ws.get(key)
     if kept is None or kept[1] < nbytes:
         ws = torch.empty((max(nbytes, 1),), dtype=torch.uint8, device=cache.device)
-        kept = cache._ws[handle] = (ws.data_ptr(), nbytes, ws)
+        kept = cache._ws[key] = (ws.data_ptr(), nbytes, ws)
     return kept[0], kept[1]
 
 

@@ -209,3 +209,42 @@ def test_first_call_of_a_host_thread(what):
         else:
             assert s.m.compact() == short.item()
         s.same()
+
+
+@pytest.mark.parametrize("alpha", [1.0, 1.5])
+def test_threads_that_share_a_stream_and_a_cache(alpha):
+    """Calls of four host threads on one stream: a call's two launches keep a workspace of their own."""
+    import threading
+    s = Server(8, 2, alpha, n_pages=120, n_seqs=8, max_pages=16, seed=8)
+    s.prompts(list(range(8)), [900, 64, 1, 700, 129, 1000, 333, 512])
+    c, E = s.c, s.E
+    work = []
+    for k in range(4):
+        ids = ints([(k + j) % 8 for j in range(3 + k)])
+        Q = s.project(3 + k)[0]
+        work.append((Q, ids, E.entmax_cache_attn(c, 1, Q, ids, 1024, alpha=alpha)))
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    results, errors = [[] for _ in work], []
+    start = threading.Barrier(len(work))
+
+    def run(k):
+        try:
+            Q, ids, _ = work[k]
+            start.wait(timeout=60)
+            for _ in range(200):
+                results[k].append(E.entmax_cache_attn(c, 1, Q, ids, 1024, alpha=alpha, stream=stream))
+        except Exception as e:  # reported below, on the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    torch.cuda.synchronize()
+    assert not errors, errors
+    for (_, _, (O, tau)), got in zip(work, results):
+        assert len(got) == 200
+        for o, t in got:
+            assert torch.equal(o, O) and torch.equal(t, tau)
